@@ -1,0 +1,124 @@
+// Internal header: activations handled eight consecutive values to a lane (an
+// "octet"), and their conversion to the output types the quantized products
+// take.  Four neighbouring lanes hold one 32-value block, so a block's largest
+// magnitude is two DPP steps away, a wave's loads and stores are contiguous,
+// and no lane walks a block by itself.
+//
+// A block that holds a NaN or an infinity is marked as a whole: scale byte 255
+// (E8M0's NaN) and zero codes, or d = NaN and zero int8 codes, so that every
+// value read from it and every product with it is NaN.
+#pragma once
+#include "common.hpp"
+
+namespace qmoe {
+
+enum ActOut { kOutF32 = 0, kOutBF16 = 1, kOutQ8 = 2, kOutMx8 = 3, kOutMx4 = 4 };
+
+QMOE_D uint32_t f32_to_bf16_bits(float v) {  // nearest even; NaN stays a NaN
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v);
+}
+QMOE_D uint32_t pack_bf16(float lo, float hi) {
+  return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
+}
+
+// eight values from a 16-byte aligned place
+template <bool BF>
+QMOE_D void load8(const void* x, size_t at, float (&v)[8]) {
+  if constexpr (BF) {
+    const uint4 q = *(const uint4*)((const uint16_t*)x + at);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
+      v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = ((const float4*)((const float*)x + at))[0];
+    const float4 b = ((const float4*)((const float*)x + at))[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+template <bool BF>
+QMOE_D void store8(void* y, size_t at, const float (&v)[8]) {
+  if constexpr (BF) {
+    *(uint4*)((uint16_t*)y + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  } else {
+    float4* p = (float4*)((float*)y + at);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// The largest |v| of a 32-value block as fp32 bits, from its four lanes (all
+// four must be active).  Bits of magnitudes compare as unsigned integers, and
+// a NaN's are above infinity's, so it is not lost as fmaxf would lose it.
+QMOE_D uint32_t block_max_bits(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
+  m = max(m, dpp_u32<0xB1, 0xF>(0u, m));  // quad_perm [1, 0, 3, 2]
+  m = max(m, dpp_u32<0x4E, 0xF>(0u, m));  // quad_perm [2, 3, 0, 1]
+  return m;
+}
+
+// Store one octet of row-major [R, K] values at flat index `at` (a multiple
+// of 8) in the output type.  Every lane of the block's four calls this.
+//  * MX: the shared exponent floor(log2 max) - emax is the exponent field of
+//    the largest magnitude less emax (zero and fp32 subnormals give byte 0);
+//    2^-E is an fp32 normal for every byte in 0..252, so scaling is exact, and
+//    the element conversions round to nearest even.  Clamping first makes
+//    them saturate; adding 0 turns a negative zero into a positive one.
+//  * int8: d = max * fp32(1 / 127), q = the quotient v / d (fp32) rounded half
+//    away from zero.
+template <int OUT>
+QMOE_D void store_act8(const float (&v)[8], size_t at, void* out, void* scales) {
+  if constexpr (OUT == kOutF32 || OUT == kOutBF16) {
+    store8<OUT == kOutBF16>(out, at, v);
+  } else {
+    const uint32_t m = block_max_bits(v);
+    const bool bad = m >= 0x7F800000u;
+    const bool first = (threadIdx.x & 3) == 0;
+    if constexpr (OUT == kOutQ8) {
+      const float d = __builtin_bit_cast(float, m) * (1.f / 127.f);
+      uint32_t w[2] = {0, 0};
+      if (d > 0.f && !bad) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float r = v[i] / d, t = truncf(r);
+          int c = (int)t + (fabsf(r - t) >= 0.5f ? (r < 0.f ? -1 : 1) : 0);
+          c = min(max(c, -127), 127);
+          w[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+        }
+      }
+      *(uint2*)((int8_t*)out + at) = make_uint2(w[0], w[1]);
+      if (first) ((float*)scales)[at >> 5] = bad ? __builtin_nanf("") : d;
+    } else {
+      constexpr int emax = OUT == kOutMx8 ? 8 : 2;
+      const int e = max((int)(m >> 23) - emax, 0);
+      const float mul = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
+      constexpr float top = OUT == kOutMx8 ? 448.f : 6.f;
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_fmed3f(v[i] * mul + 0.f, -top, top);
+      if constexpr (OUT == kOutMx8) {
+        int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+        w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w0, true);
+        int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
+        w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], w1, true);
+        *(uint2*)((uint8_t*)out + at) = make_uint2(bad ? 0 : w0, bad ? 0 : w1);
+      } else {
+        uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, t[0], t[1], 1.f, 0);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[2], t[3], 1.f, 1);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[4], t[5], 1.f, 2);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[6], t[7], 1.f, 3);
+        *(uint32_t*)((uint8_t*)out + (at >> 1)) = bad ? 0 : w;
+      }
+      if (first) ((uint8_t*)scales)[at >> 5] = (uint8_t)(bad ? 255 : e);
+    }
+  }
+}
+
+}  // namespace qmoe

@@ -71,6 +71,9 @@ _SIGNATURES = {
     "qgemv_q8_0_i8": (_I, [_VP, _I, _I, _VP, _VP, _I, _VP, _VP]),
     "qgemm_mxfp4_mxfp8": (_I, [_VP, _I, _I, _VP, _VP, _I, _VP, _VP]),
     "qgemm_q8_0_i8": (_I, [_VP, _I, _I, _VP, _VP, _I, _VP, _VP]),
+    "qquantize_act_mxfp4": (_I, [_VP, _I, _I, _I, _VP, _VP, _VP]),
+    "qdequant_act_mxfp4": (_I, [_VP, _VP, _I, _I, _VP, _I, _VP]),
+    "qgemm_mxfp4_mxfp4": (_I, [_VP, _I, _I, _VP, _VP, _I, _VP, _I, _VP]),
     "moe_layer_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "moe_layer_decode": (_I, [ctypes.POINTER(Tier), _I, _I, _I, _I, _VP, _I, _I, _VP, _VP, _I,
                               _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
@@ -86,6 +89,12 @@ for _f in FORMATS:
     _SIGNATURES[f"qquantize_{_f}"] = (_I, [_VP, _I, _I, _VP, _VP])
     _SIGNATURES[f"qdequant_{_f}"] = (_I, [_VP, _I, _I, _VP, _VP])
     _SIGNATURES[f"qgemv_{_f}"] = (_I, [_VP, _I, _I, _VP, _I, _I, _VP, _VP])
+_NORM_ARGS = [_VP, _I, _VP, _VP, _I, _VP, ctypes.c_double, _I, _I]
+_SIGNATURES["qnorm"] = (_I, _NORM_ARGS + [_VP, _I, _VP])
+for _f in ("q8", "mxfp8", "mxfp4"):
+    _SIGNATURES[f"qnorm_act_{_f}"] = (_I, _NORM_ARGS + [_VP, _VP, _VP])
+    _SIGNATURES[f"qswiglu_act_{_f}"] = (_I, [_VP, _VP, _I, ctypes.c_longlong, _I, _I, _VP, _VP,
+                                             _VP])
 _SIGNATURES["qgemv_batch"] = (_I, [_VP, _I, _VP])
 
 
@@ -457,6 +466,182 @@ def gemm_mxfp4_mxfp8(W, N, K, codes, scales, out=None):
         out = torch.empty((R, N), dtype=torch.float32, device=codes.device)
     _check(lib().qgemm_mxfp4_mxfp8(_p(W), N, K, _p(codes), _p(scales), R, _p(out), _stream()),
            "qgemm_mxfp4_mxfp8")
+    return out
+
+
+# ---------------------------------------------------- 4-bit activations --
+
+ACT_FORMATS = ("q8", "mxfp8", "mxfp4")
+
+
+def _same_device(*ts):
+    """The one GPU that all the given tensors (None skipped) live on."""
+    ts = [t for t in ts if t is not None]
+    for t in ts:
+        _need(t.is_cuda, "tensors must be CUDA tensors")
+    dev = ts[0].device
+    _need(all(t.device == dev for t in ts), "tensors must be on one device")
+    return dev
+
+
+def _launch(name, dev, *args):
+    """Call entry point `name` with its device current, on that device's
+    current stream."""
+    torch = _torch()
+    if dev.index == torch.cuda.current_device():
+        _check(getattr(lib(), name)(*args, _stream()), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(lib(), name)(*args, _stream()), name)
+
+
+def _out_dtype(dtype):
+    torch = _torch()
+    _need(dtype in (torch.float32, torch.bfloat16), f"outputs are float32 or bfloat16, not {dtype}")
+    return F32 if dtype == torch.float32 else BF16
+
+
+def _matrix(t, shape, dtype, what):
+    _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.is_contiguous(),
+          f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _act_out(fmt, R, K, dev, out):
+    """(codes, scales) tensors of activation format `fmt` for [R, K]."""
+    torch = _torch()
+    _need(fmt in ACT_FORMATS, f"activation format {fmt!r} is not one of {ACT_FORMATS}")
+    _need(K > 0 and K % 32 == 0, f"K={K} is not a multiple of 32")
+    kinds = {"q8": (K, torch.int8, torch.float32), "mxfp8": (K, torch.uint8, torch.uint8),
+             "mxfp4": (K // 2, torch.uint8, torch.uint8)}
+    width, ct, st = kinds[fmt]
+    if out is None:
+        return (torch.empty((R, width), dtype=ct, device=dev),
+                torch.empty((R, K // 32), dtype=st, device=dev))
+    _matrix(out[0], (R, width), ct, "codes")
+    _matrix(out[1], (R, K // 32), st, "scales")
+    return out
+
+
+def quantize_act_mxfp4(x, out=None):
+    """Activations [R, K] (float32 or bfloat16) -> MXFP4 codes [R, K/2] uint8
+    (two E2M1 codes per byte, low nibble first) and scales [R, K/32] uint8
+    (E8M0)."""
+    _need(x.dim() == 2, "x must be [R, K]")
+    _cuda_contig(x)
+    R, K = x.shape
+    codes, scales = _act_out("mxfp4", R, K, x.device, out)
+    dev = _same_device(x, codes, scales)
+    _launch("qquantize_act_mxfp4", dev, _p(x), _dtype_code(x), R, K, _p(codes), _p(scales))
+    return codes, scales
+
+
+def dequantize_act_mxfp4(codes, scales, dtype=None, out=None):
+    """The values [R, K] of MXFP4 activations (float32 unless dtype says
+    bfloat16)."""
+    torch = _torch()
+    R, K = codes.shape[0], 2 * codes.shape[1]
+    _matrix(codes, (R, K // 2), torch.uint8, "codes")
+    _matrix(scales, (R, K // 32), torch.uint8, "scales")
+    if out is None:
+        dtype = torch.float32 if dtype is None else dtype
+        _out_dtype(dtype)
+        out = torch.empty((R, K), dtype=dtype, device=codes.device)
+    else:
+        _matrix(out, (R, K), out.dtype if dtype is None else dtype, "out")
+    dev = _same_device(codes, scales, out)
+    _launch("qdequant_act_mxfp4", dev, _p(codes), _p(scales), R, K, _p(out),
+            _out_dtype(out.dtype))
+    return out
+
+
+def _norm_args(x, w, eps, res, res_out):
+    torch = _torch()
+    _need(x.dim() == 2, "x must be [R, K]")
+    R, K = x.shape
+    _cuda_contig(x, w, res, res_out)
+    _matrix(w, (K,), torch.float32, "w")
+    code = 0
+    if res is not None:
+        code = _dtype_code(res)
+        _matrix(res, (R, K), res.dtype, "res")
+        if res_out is None:
+            res_out = torch.empty_like(res)
+        _matrix(res_out, (R, K), res.dtype, "res_out")
+    else:
+        _need(res_out is None, "res_out without res")
+    dev = _same_device(x, w, res, res_out)
+    args = (_p(x), _dtype_code(x), _p(res), _p(res_out), code, _p(w), float(eps), R, K)
+    return dev, R, K, res_out, args
+
+
+def norm(x, w, eps, res=None, res_out=None, dtype=None, out=None):
+    """RMS norm of the rows of x [R, K], or of h = x + res: y = h * w /
+    sqrt(mean(h^2) + eps) in float32, or dtype.  Returns y, with res (y, h);
+    h has res' type and goes to res_out (a new tensor unless given; res itself
+    for an update in place)."""
+    torch = _torch()
+    dev, R, K, h, args = _norm_args(x, w, eps, res, res_out)
+    if out is None:
+        dtype = torch.float32 if dtype is None else dtype
+        _out_dtype(dtype)
+        out = torch.empty((R, K), dtype=dtype, device=dev)
+    else:
+        _matrix(out, (R, K), out.dtype if dtype is None else dtype, "out")
+        _same_device(x, out)
+    _launch("qnorm", dev, *args, _p(out), _out_dtype(out.dtype))
+    return out if res is None else (out, h)
+
+
+def norm_act(fmt, x, w, eps, res=None, res_out=None, out=None):
+    """norm's float32 rows in activation format fmt ("q8", "mxfp8", "mxfp4"):
+    (codes, scales), with res (codes, scales, h)."""
+    dev, R, K, h, args = _norm_args(x, w, eps, res, res_out)
+    codes, scales = _act_out(fmt, R, K, dev, out)
+    _same_device(x, codes, scales)
+    _launch(f"qnorm_act_{fmt}", dev, *args, _p(codes), _p(scales))
+    return (codes, scales) if res is None else (codes, scales, h)
+
+
+def swiglu_act(fmt, gate, up, out=None):
+    """gate / (1 + exp(-gate)) * up [R, K] in activation format fmt: (codes,
+    scales).  gate and up are float32 or bfloat16, with contiguous rows; the
+    rows may lie further apart (the two halves of one [R, 2K] tensor)."""
+    _need(gate.dim() == 2 and gate.shape == up.shape and gate.dtype == up.dtype,
+          "gate and up must be [R, K] of one type")
+    R, K = gate.shape
+    dev = _same_device(gate, up)
+    ld = K
+    if R > 1:
+        ld = gate.stride(0)
+        _need(gate.stride(1) == up.stride(1) == 1 and up.stride(0) == ld,
+              "gate and up must have contiguous rows, equally far apart")
+    else:
+        _need(R == 0 or gate.stride(1) == up.stride(1) == 1, "gate and up must have contiguous rows")
+    codes, scales = _act_out(fmt, R, K, dev, out)
+    _same_device(gate, codes, scales)
+    _launch(f"qswiglu_act_{fmt}", dev, _p(gate), _p(up), _dtype_code(gate), ld, R, K, _p(codes),
+            _p(scales))
+    return codes, scales
+
+
+def gemm_mxfp4_mxfp4(W, N, K, codes, scales, dtype=None, out=None):
+    """y [R, N] (float32 unless dtype says bfloat16) = W (MXFP4 [N, K]) times
+    the MXFP4 activations; R from one decode row to a prefill chunk."""
+    torch = _torch()
+    R = codes.shape[0]
+    _matrix(codes, (R, K // 2), torch.uint8, "codes")
+    _matrix(scales, (R, K // 32), torch.uint8, "scales")
+    _need(W.dtype == torch.uint8 and W.is_contiguous() and W.numel() >= tensor_bytes("mxfp4", N, K),
+          "W must be a packed MXFP4 [N, K] tensor")
+    if out is None:
+        dtype = torch.float32 if dtype is None else dtype
+        _out_dtype(dtype)
+        out = torch.empty((R, N), dtype=dtype, device=codes.device)
+    else:
+        _matrix(out, (R, N), out.dtype if dtype is None else dtype, "out")
+    dev = _same_device(W, codes, scales, out)
+    _launch("qgemm_mxfp4_mxfp4", dev, _p(W), N, K, _p(codes), _p(scales), R, _p(out),
+            _out_dtype(out.dtype))
     return out
 
 

@@ -381,6 +381,78 @@ int qgemv_q8_0_i8(const void *W, int N, int K, const int8_t *q, const float *d,
 int qgemm_q8_0_i8(const void *W, int N, int K, const int8_t *q, const float *d,
                   int R, float *y, void *stream);
 
+/* ----------------------------- 4-bit activations, and what feeds them ----
+ * The dense layer with both operands in 4 bits ([P1] "NInfer 80 SM port", list
+ * of hardware limits: W4A4 matrix ops), from the residual stream to the next
+ * norm: qnorm_act_* -> product (gate and up) -> qswiglu_act_* -> product (down).
+ *
+ * Activation formats (K % 32 == 0, one scale per 32 values along K):
+ *   q8    q [R, K] int8, d [R, K/32] fp32          as qquantize_act_q8, except
+ *         that d = max|x| * fp32(1/127), one rounding more than max|x| / 127
+ *   mxfp8 codes [R, K] E4M3, scales [R, K/32] E8M0  as qquantize_act_mxfp8
+ *   mxfp4 codes [R, K/2] E2M1 (low nibble first), scales [R, K/32] E8M0:
+ *         E = floor(log2 max|x|) - 2, stored as E + 127 (at least 0; 0 for an
+ *         all-zero block); code = nearest E2M1 to x / 2^E, ties to even,
+ *         saturating at 6, sign bit = (x < 0): qquantize_mxfp4's rule.
+ * In the functions of this section a block that holds a NaN or an infinity
+ * gets scale 255 (E8M0 NaN) and codes 0, or d = NaN and q = 0: whatever is
+ * read back or multiplied from it is NaN.
+ *
+ * qquantize_act_mxfp4: x [R, K] (x_dtype) -> codes, scales.  x and codes
+ *   16-byte aligned.
+ * qdequant_act_mxfp4: codes, scales -> y [R, K] (y_dtype); exact in both types
+ *   but for magnitudes outside the type's range (scale 255: NaN).
+ *   codes and y 16-byte aligned.
+ * R * K < 2^35 for both (UNSUPPORTED beyond).
+ *
+ * qnorm: RMS norm of rows, with the residual's addition:
+ *     h = x + res   (fp32 sum, rounded to res_dtype, stored to res_out)
+ *     h = x         when res is NULL (res_out must be NULL too)
+ *     y = h * w / sqrt(mean_k h^2 + eps), rounded to fp32, then to y_dtype
+ *   The sum, the root and the product are fp64, so y's fp32 value is the
+ *   correctly rounded one (but for values within 2^-50 of a rounding border).
+ *   x [R, K] (x_dtype), res and res_out [R, K] (res_dtype, ignored without
+ *   res), w [K] fp32, y [R, K].  res_out may be NULL, or res itself (in
+ *   place); no other output may overlap an input.
+ * qnorm_act_<fmt>: the activation quantizer of <fmt> applied to the fp32 y.
+ *   All pointers 16-byte aligned (mxfp scales: any; d: 4-byte).
+ *   Limits: K <= 32768, K % 32 == 0 (qnorm: K % 8 == 0), eps >= 0.
+ *
+ * qswiglu_act_<fmt>: the activation quantizer of <fmt> applied to
+ *     v = gate / (1 + exp(-gate)) * up, in fp64, rounded once to fp32
+ *   gate and up [R, K] (x_dtype) with rows ld values apart (ld >= K,
+ *   ld % 8 == 0): two matrices, or the halves of one [R, 2K].  gate, up and
+ *   codes 16-byte aligned.  R * K < 2^35.
+ *
+ * qgemm_mxfp4_mxfp4: y [R, N] (y_dtype) = sum_k w[n, k] * x[r, k] for MXFP4
+ *   weights W [N, K] (qmoe layout, 256-byte aligned) and MXFP4 activations;
+ *   products are exact, sums are fp32 in the matrix cores, rounded once to
+ *   y_dtype.  Any R and N; K % 32 == 0, K <= 65536.  codes and y 16-byte
+ *   aligned, scales any.
+ * Errors: INVALID_ARG for sizes, null pointers and misalignment; UNSUPPORTED
+ *   for unknown dtypes and sizes beyond a limit.                             */
+#define QMOE_NORM_ARGS                                                          \
+  const void *x, int x_dtype, const void *res, void *res_out, int res_dtype,    \
+      const float *w, double eps, int R, int K
+int qquantize_act_mxfp4(const void *x, int x_dtype, int R, int K,
+                        uint8_t *codes, uint8_t *scales, void *stream);
+int qdequant_act_mxfp4(const uint8_t *codes, const uint8_t *scales, int R, int K,
+                       void *y, int y_dtype, void *stream);
+int qnorm(QMOE_NORM_ARGS, void *y, int y_dtype, void *stream);
+int qnorm_act_q8(QMOE_NORM_ARGS, int8_t *q, float *d, void *stream);
+int qnorm_act_mxfp8(QMOE_NORM_ARGS, uint8_t *codes, uint8_t *scales, void *stream);
+int qnorm_act_mxfp4(QMOE_NORM_ARGS, uint8_t *codes, uint8_t *scales, void *stream);
+#undef QMOE_NORM_ARGS
+int qswiglu_act_q8(const void *gate, const void *up, int x_dtype, long long ld,
+                   int R, int K, int8_t *q, float *d, void *stream);
+int qswiglu_act_mxfp8(const void *gate, const void *up, int x_dtype, long long ld,
+                      int R, int K, uint8_t *codes, uint8_t *scales, void *stream);
+int qswiglu_act_mxfp4(const void *gate, const void *up, int x_dtype, long long ld,
+                      int R, int K, uint8_t *codes, uint8_t *scales, void *stream);
+int qgemm_mxfp4_mxfp4(const void *W, int N, int K, const uint8_t *codes,
+                      const uint8_t *scales, int R, void *y, int y_dtype,
+                      void *stream);
+
 /* moe_layer_decode: the whole routed-expert layer of a decode step in one
  * launch ([P2] "瓶颈分析": router top-k over the experts, the selected
  * experts' SwiGLU FFNs, their weighted sum; "优化策略二/三": tiers of mixed

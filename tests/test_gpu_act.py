@@ -1,0 +1,248 @@
+"""RMS norm with residual and quantized output, SwiGLU with quantized output,
+the MXFP4 activation quantizer and its read-back: every output bit for bit
+against the extended-precision oracle."""
+import numpy as np
+import pytest
+
+from gpu_util import requires_gpu, to_gpu, to_np, assert_bitexact, torch
+from oracle import act
+from oracle import formats as fm
+from decode_moe_mul_amd import qmoe, synth
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+FMTS = qmoe.ACT_FORMATS
+
+
+def _x(shape, seed, sigma=1.0, bf=False):
+    x = synth.normal(shape, sigma, seed, synth.ACT, shape[0])
+    return synth.bf16_round(x) if bf else x
+
+
+def _dev(x, bf):
+    return to_gpu(x).to(torch.bfloat16) if bf else to_gpu(x)
+
+
+def _same_act(got, want, what=""):
+    q, s = to_np(got[0]), to_np(got[1])
+    assert s.shape == want[1].shape and q.shape == want[0].shape
+    same = (s == want[1]) | ((s != s) & (want[1] != want[1]))
+    assert same.all(), f"{what}: {(~same).sum()} scales differ"
+    assert (q == want[0]).all(), f"{what}: {(q != want[0]).sum()} code bytes differ"
+
+
+# --------------------------------------------------------------- MXFP4 --
+
+def _special():
+    x = np.zeros((8, 64), np.float32)
+    grid = fm.e2m1_value(np.arange(8))
+    mids = (grid[:-1] + grid[1:]) / 2
+    x[0, :8], x[0, 8:15], x[0, 15:22] = grid, mids, -mids      # every tie
+    x[0, 32:] = -x[0, :32] * 2.0 ** -30
+    x[1, :4] = [7.99, 6.5, 5.0, 7.0]                           # saturates at 6
+    x[2] = -0.0
+    x[3] = np.linspace(-3e-38, 3e-38, 64, dtype=np.float32)    # around the normal floor
+    x[4] = np.float32(1e-45) * np.arange(64)                   # fp32 subnormals
+    x[5, ::2] = 3.4e38
+    x[6, 1] = np.nextafter(np.float32(4), np.float32(0))       # one step below a power of two
+    x[7, 40] = 1e-30
+    return x
+
+
+def test_mxfp4_special_values():
+    x = _special()
+    _same_act(qmoe.quantize_act_mxfp4(to_gpu(x)), act.quantize("mxfp4", x))
+
+
+@pytest.mark.parametrize("R,K", [(1, 32), (3, 96), (6, 2048), (5, 14336), (257, 160), (2, 65568)])
+@pytest.mark.parametrize("bf", [False, True], ids=["f32", "bf16"])
+def test_mxfp4_quantizer_and_read_back(R, K, bf):
+    x = _x((R, K), 3, bf=bf)
+    got = qmoe.quantize_act_mxfp4(_dev(x, bf))
+    want = act.quantize("mxfp4", x)
+    _same_act(got, want)
+    v = act.dequantize_mxfp4(*act.quantize_mxfp4(x))
+    assert_bitexact(to_np(qmoe.dequantize_act_mxfp4(*got)), v)
+    assert_bitexact(to_np(qmoe.dequantize_act_mxfp4(*got, dtype=torch.bfloat16).float()), v)
+
+
+def test_mxfp4_codes_are_the_weights_quantizers():
+    N, K = 33, 2048
+    x = to_gpu(_x((N, K), 4, 0.02))
+    codes, scales = qmoe.quantize_act_mxfp4(x)
+    W, off = qmoe.quantize("mxfp4", x), qmoe.plane_offsets("mxfp4", N, K)
+    assert torch.equal(codes.view(-1), W[:N * K // 2])
+    assert torch.equal(scales.view(-1), W[off[1]:off[1] + N * K // 32])
+
+
+def test_read_back_of_every_code_and_scale():
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 2))
+    e = np.arange(256, dtype=np.uint8)[:, None]
+    y = to_np(qmoe.dequantize_act_mxfp4(to_gpu(act.pack_codes(codes)), to_gpu(e)))
+    with np.errstate(over="ignore"):
+        assert_bitexact(y, act.dequantize_mxfp4(codes, e).astype(np.float32))
+
+
+# ---------------------------------------------------------------- norm --
+
+# one octet per thread, several waves a row, rows not a multiple of a block's,
+# two and four octets per thread, several rows to a block in turn
+SIZES = [(1, 32), (1, 4096), (3, 96), (5, 2080), (300, 2048), (2, 7168), (3, 8224), (2, 16416),
+         (1, 32768), (1100, 160), (2100, 2080), (1031, 8224), (4500, 32)]
+
+
+@pytest.mark.parametrize("R,K", SIZES)
+@pytest.mark.parametrize("fmt", ("f32", "bf16") + FMTS)
+def test_norm_sizes(R, K, fmt):
+    x, res = _x((R, K), 5), _x((R, K), 6, 3.0, bf=True)
+    w = 1 + _x((1, K), 7, 0.1)[0]
+    y, h = act.rms_norm(x, w, 1e-5, res, res_bf16=True)
+    gx, gw, gr = to_gpu(x), to_gpu(w), _dev(res, True)
+    if fmt in FMTS:
+        got = qmoe.norm_act(fmt, gx, gw, 1e-5, res=gr)
+        _same_act(got, act.quantize(fmt, y), f"{fmt} {R}x{K}")
+        gh = got[2]
+    else:
+        gy, gh = qmoe.norm(gx, gw, 1e-5, res=gr,
+                           dtype=torch.float32 if fmt == "f32" else torch.bfloat16)
+        assert_bitexact(to_np(gy.float()), y if fmt == "f32" else act.bf16(y))
+    assert gh.dtype == torch.bfloat16
+    assert_bitexact(to_np(gh.float()), h, "h")
+
+
+@pytest.mark.parametrize("xbf", [False, True], ids=["x_f32", "x_bf16"])
+@pytest.mark.parametrize("res", ["none", "f32", "bf16"])
+@pytest.mark.parametrize("fmt", ("f32", "bf16") + FMTS)
+def test_norm_types(xbf, res, fmt):
+    for R, K in ((7, 288), (1027, 288)):
+        x, r = _x((R, K), 8, bf=xbf), _x((R, K), 9, 3.0, bf=res == "bf16")
+        w = 1 + _x((1, K), 7, 0.1)[0]
+        gx, gw = _dev(x, xbf), to_gpu(w)
+        gr = None if res == "none" else _dev(r, res == "bf16")
+        y, h = act.rms_norm(x, w, 1e-6, None if res == "none" else r, res == "bf16")
+        if fmt in FMTS:
+            got = qmoe.norm_act(fmt, gx, gw, 1e-6, res=gr, res_out=gr)   # in place
+            _same_act(got, act.quantize(fmt, y))
+        else:
+            dt = torch.float32 if fmt == "f32" else torch.bfloat16
+            got = qmoe.norm(gx, gw, 1e-6, res=gr, res_out=gr, dtype=dt)
+            got = got if gr is not None else (got,)
+            assert_bitexact(to_np(got[0].float()), y if fmt == "f32" else act.bf16(y))
+        if gr is not None:
+            assert got[-1] is gr
+            assert_bitexact(to_np(gr.float()), h)
+
+
+def test_plain_norm_of_a_width_that_is_no_multiple_of_32():
+    x, w = _x((5, 1000), 10), 1 + _x((1, 1000), 11, 0.1)[0]
+    assert_bitexact(to_np(qmoe.norm(to_gpu(x), to_gpu(w), 1e-5)), act.rms_norm(x, w, 1e-5)[0])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_norm_rows_of_zeros_huge_tiny_and_non_finite_values(fmt):
+    K = 256
+    x = _x((8, K), 12)
+    x[1] = 0.0
+    x[2] *= np.float32(1e30)       # squares beyond fp32
+    x[3] *= np.float32(1e-30)      # squares below fp32
+    x[4, 77] = np.nan
+    x[5, 200] = np.inf
+    w = np.ones(K, np.float32)
+    y = act.rms_norm(np.where(np.isfinite(x), x, 0), w, 1e-5)[0]
+    y[4:6] = np.nan                # the row's norm is NaN or infinite: 0 or NaN times it
+    q, s = (to_np(t) for t in qmoe.norm_act(fmt, to_gpu(x), to_gpu(w), 1e-5))
+    wq, ws = act.quantize(fmt, y)
+    keep = [0, 1, 2, 3, 6, 7]
+    assert (q[keep] == wq[keep]).all() and (s[keep] == ws[keep]).all()
+    bad = np.isnan(s) if fmt == "q8" else s == 255
+    assert bad[4].all()
+    assert bad[5, 200 // 32]       # inf * (1 / inf) is NaN; its neighbours are 0
+    assert not bad[keep].any()
+
+
+# -------------------------------------------------------------- SwiGLU --
+
+@pytest.mark.parametrize("R,K", [(1, 32), (3, 96), (16, 14336), (130, 640), (1, 65536)])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bf", [False, True], ids=["f32", "bf16"])
+@pytest.mark.parametrize("joint", [False, True], ids=["separate", "halves"])
+def test_swiglu(R, K, fmt, bf, joint):
+    gu = _x((R, 2 * K), 13, 1.5, bf=bf)
+    g, u = gu[:, :K], gu[:, K:]
+    d = _dev(gu, bf)
+    gg, uu = d[:, :K], d[:, K:]
+    if not joint:
+        gg, uu = gg.contiguous(), uu.contiguous()
+    _same_act(qmoe.swiglu_act(fmt, gg, uu), act.quantize(fmt, act.swiglu(g, u)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_swiglu_far_values(fmt):
+    g = np.zeros((4, 64), np.float32)
+    g[0] = np.linspace(-120, 120, 64)
+    g[1] = np.linspace(-3e38, 3e38, 64)
+    g[2] = np.linspace(-1e-38, 1e-38, 64)
+    g[3] = -np.linspace(80, 110, 64)
+    u = np.where(np.arange(64) % 2, -1.0, 1.0).astype(np.float32) * np.ones((4, 1), np.float32)
+    _same_act(qmoe.swiglu_act(fmt, to_gpu(g), to_gpu(u)), act.quantize(fmt, act.swiglu(g, u)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_swiglu_marks_non_finite_blocks(fmt):
+    g, u = _x((3, 96), 14), _x((3, 96), 15)
+    g[0, 3], u[1, 40], g[2, 95] = np.nan, np.inf, np.inf
+    _, s = qmoe.swiglu_act(fmt, to_gpu(g), to_gpu(u))
+    s = to_np(s)
+    bad = np.isnan(s) if fmt == "q8" else s == 255
+    want = np.zeros((3, 3), bool)
+    want[0, 0] = want[1, 1] = want[2, 2] = True
+    assert (bad == want).all()
+
+
+# ------------------------------------------- streams, graphs, empty calls --
+
+def test_empty_calls():
+    x = torch.empty((0, 64), device="cuda")
+    w = torch.ones(64, device="cuda")
+    assert qmoe.norm(x, w, 1e-5).shape == (0, 64)
+    for fmt in FMTS:
+        assert qmoe.norm_act(fmt, x, w, 1e-5, res=x)[1].shape == (0, 2)
+        assert qmoe.swiglu_act(fmt, x, x)[1].shape == (0, 2)
+    assert qmoe.dequantize_act_mxfp4(*qmoe.quantize_act_mxfp4(x)).shape == (0, 64)
+
+
+def test_values_behind_the_last_row_stay():
+    R, K = 3, 96
+    x, w = to_gpu(_x((R, K), 16)), torch.ones(K, device="cuda")
+    for fmt in FMTS:
+        want = qmoe.norm_act(fmt, x, w, 1e-5)
+        big = [torch.full((R + 2,) + t.shape[1:], 77, dtype=t.dtype, device="cuda") for t in want]
+        qmoe.norm_act(fmt, x, w, 1e-5, out=(big[0][:R], big[1][:R]))
+        for b, t in zip(big, want):
+            assert torch.equal(b[:R], t) and (b[R:] == 77).all()
+
+
+def test_graph_replays_and_another_stream():
+    R, K = 6, 2048
+    x, res = to_gpu(_x((R, K), 17)), to_gpu(_x((R, K), 18))
+    w = torch.ones(K, device="cuda")
+
+    def step():
+        c, s, h = qmoe.norm_act("mxfp4", x, w, 1e-5, res=res)
+        c2, s2 = qmoe.swiglu_act("mxfp8", h, x)
+        return c, s, h, c2, s2, qmoe.dequantize_act_mxfp4(c, s)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for a, b in zip(step(), [t.clone() for t in step()]):
+            assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for seed in (19, 20, 21):
+        x.copy_(to_gpu(_x((R, K), seed)))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, step()):
+            assert torch.equal(a, b)
