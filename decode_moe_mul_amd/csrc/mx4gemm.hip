@@ -14,6 +14,7 @@
 // codes are then 64 consecutive bytes of the row and its four scales one
 // 32-bit word, whose byte s serves step s without any repacking.
 #include <algorithm>
+#include <type_traits>
 
 #include "act.hpp"
 
@@ -149,6 +150,353 @@ static int launch_rows(const Mx4Params& P, bool ybf, hipStream_t s) {
   return QMOE_LAUNCH("mxfp4_rows", (mxfp4_rows_kernel<RT, false>), grid, 64 * waves, lds, s, P);
 }
 
+// ------------------------------------------------------ many rows ------
+// A block computes BM = 32 WR TM activation rows x BN = 32 WC TN weight rows
+// with WR x WC waves of TM x TN 32x32x64 ops.  A step is 256 values of K, 128
+// code bytes of a row: four groups of ops, lane 32 h + i of group s taking block
+// 2 s + h of row i.
+//
+// A SIMD holds one wave (its sums fill half the registers), so whatever that
+// wave waits for, the matrix core waits for too.  Everything else is therefore
+// issued between matrix ops, in an order that the compiler keeps:
+//  * codes go from memory to LDS without passing registers (16 bytes a lane,
+//    1 KB of LDS, 8 rows of 128 bytes, each a whole cache line: half lines
+//    doubled the requests to L2, which then set the pace), into one of two
+//    buffers, a step ahead;
+//  * the operands of a group are read from LDS during the group before it; the
+//    step's barrier stands before its last group, when every wave holds the
+//    rest of the step's operands, and frees the step's buffer;
+//  * scales pass through registers (their rows have any alignment): 16 bytes a
+//    row serve two steps, in one of two LDS buffers; a byte permute gives each
+//    lane its four blocks of a step in one word, whose bytes the ops select.
+// The 16-byte chunk c of tile row q lies at chunk c ^ (q & 7), chosen by
+// which chunk of memory a lane fetches, so that the rows one operand read
+// touches spread over the banks.  Rows past the ends repeat the last one and
+// are never stored; blocks past K's end repeat the row's last one, and zeros
+// replace the activations'.
+template <int WR_, int WC_, int TM_, int TN_>
+struct Tile {
+  static constexpr int WR = WR_, WC = WC_, TM = TM_, TN = TN_;
+  static constexpr int BM = 32 * WR * TM, BN = 32 * WC * TN, ROWS = BM + BN, NW = WR * WC;
+  static constexpr int THREADS = 64 * NW;
+  static constexpr int CODES = ROWS * 128, SCALES = ROWS * 16;  // bytes of one buffer
+  static constexpr size_t LDS = 2 * (CODES + SCALES);
+  static constexpr int JA = BM / 8 / NW, J = ROWS / 8 / NW;     // copies per wave and step
+  static constexpr int SR = (ROWS + THREADS - 1) / THREADS;     // scale rows per thread
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && J % 2 == 0, "");
+};
+
+typedef float v16f_t __attribute__((ext_vector_type(16)));
+
+template <int SEL>
+QMOE_D v16f_t mma4_32(uint4 a, uint32_t sa, uint4 b, uint32_t sb, v16f_t c) {
+  const v8i_t av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i_t bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, SEL, (int)sa, SEL,
+                                                         (int)sb);
+}
+
+// a block-uniform address in scalar registers
+QMOE_D const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t a = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+  return (const uint8_t*)((uint64_t)hi << 32 | lo);
+}
+
+// 16 bytes a lane from base + off to LDS address lds + 16 * lane.  It has no
+// output register; its completion is counted with the vector loads, in order,
+// and waited for by wait_copies before the barrier that hands the data over.
+// The compiler does not count it: its own waits for vector loads can only be
+// longer than needed.
+QMOE_D void copy_to_lds(uint32_t lds, const uint8_t* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(base)
+               : "memory");
+}
+QMOE_D void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <class T, bool YBF>
+__global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int tiles_m,
+                                                                int tiles_n) {
+  constexpr int TM = T::TM, TN = T::TN, M = TM * TN, NR = TM + TN;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Blocks are dealt to the 8 XCDs in turn: give each XCD one run of tiles,
+  // down the rows first, so that its L2 serves both operands' reuse.
+  const int T_ = tiles_m * tiles_n, per = T_ >> 3, extra = T_ & 7;
+  const int x = blockIdx.x & 7;
+  const int tile = x * per + min(x, extra) + (blockIdx.x >> 3);
+  const int r0 = (tile % tiles_m) * T::BM, n0 = (tile / tiles_m) * T::BN;
+  const int nb = P.K >> 5, steps = (nb + 7) >> 3, turns = (nb + 15) >> 4;
+  const uint32_t rowb = (uint32_t)P.K >> 1;
+  const uint8_t* const abase = P.xq + (size_t)r0 * rowb;
+  const uint8_t* const bbase = P.wq + (size_t)n0 * rowb;
+  const int arows = P.R - r0 - 1, brows = P.N - n0 - 1;  // last valid row of the tile
+
+  // This lane's source offset of each copy: copy j of the wave fills tile rows
+  // 8 (wave + NW j) .. + 7, so the lane's chunk is the same for every j.
+  const int rem = nb - 8 * (steps - 1);  // blocks of the last step, 1..8
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const uint32_t over = 16u * (uint32_t)max(chunk - (rem - 1), 0);
+  uint32_t off[T::J];
+#pragma unroll
+  for (int j = 0; j < T::J; ++j) {
+    const int q = 8 * (wave + T::NW * j) + (lane >> 3);
+    const int row = j < T::JA ? min(q, arows) : min(q - T::BM, brows);
+    off[j] = (uint32_t)row * rowb + 16u * (uint32_t)chunk;
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const auto copy = [&](int st, int j) {
+    copy_to_lds(lds0 + (st & 1) * T::CODES + (wave + T::NW * j) * 1024,
+                uniform((j < T::JA ? abase : bbase) + (size_t)st * 128),
+                off[j] - (st + 1 == steps ? over : 0));
+  };
+  // scales of turn u (16 blocks), tile row q at 16 q; zeros past the row's end
+  uint8_t* const sc = smem + 2 * T::CODES;
+  uint4 sreg[T::SR];
+  const auto load_scales = [&](int u) {
+#pragma unroll
+    for (int j = 0; j < T::SR; ++j) {
+      const int q = tid + j * T::THREADS;
+      const uint8_t* p = (q < T::BM ? P.xs + (size_t)(r0 + min(q, arows)) * nb
+                                    : P.ws + (size_t)(n0 + min(q - T::BM, brows)) * nb) + 16 * u;
+      if (16 * u + 16 <= nb) {
+        __builtin_memcpy(&sreg[j], p, 16);
+      } else {
+        uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+        for (int b = nb - 16 * u - 1; b >= 0; --b) {
+          hi = hi << 8 | lo >> 56;
+          lo = lo << 8 | p[b];
+        }
+        sreg[j] = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+      }
+    }
+  };
+  const auto store_scales = [&](int u) {
+#pragma unroll
+    for (int j = 0; j < T::SR; ++j) {
+      const int q = tid + j * T::THREADS;
+      if (T::ROWS % T::THREADS == 0 || q < T::ROWS)
+        *(uint4*)(sc + (u & 1) * T::SCALES + q * 16) = sreg[j];
+    }
+  };
+  // the blocks past K's end in the last step: zeros for the activations
+  const auto clear_tail = [&]() {
+    uint8_t* buf = smem + ((steps - 1) & 1) * T::CODES;
+    for (int q = tid; q < T::BM; q += T::THREADS)
+      for (int c = rem; c < 8; ++c)
+        *(uint4*)(buf + q * 128 + 16 * (c ^ (q & 7))) = make_uint4(0, 0, 0, 0);
+  };
+
+  const int wm = (wave / T::WC) * 32 * TM, wn = (wave % T::WC) * 32 * TN;
+  const int qa = wm + i, qb = T::BM + wn + i;  // the lane's rows of the first ops
+  v16f_t acc[TM][TN];
+#pragma unroll
+  for (int m = 0; m < TM; ++m)
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[m][n][j] = 0.f;
+
+  struct Ops {
+    uint4 v[NR];  // TM activation rows, then TN weight rows
+  };
+  struct Scl {
+    uint32_t v[NR];
+  };
+  // operands in the order the ops use them: a0, b0 .. , a1 ..
+  const auto nth = [](int r) { return r == 0 ? 0 : r <= TN ? TM + r - 1 : r - TN; };
+  const auto row_of = [&](int r) { return r < TM ? qa + 32 * r : qb + 32 * (r - TM); };
+  const auto read_op = [&](int st, int s, int r, Ops& o) {
+    o.v[r] = *(const uint4*)(smem + (st & 1) * T::CODES + row_of(r) * 128 +
+                             16 * ((2 * s + h) ^ (i & 7)));
+  };
+  uint2 raw[NR];  // a row's scales of the next step
+  const auto read_raw = [&](int st, int r) {
+    raw[r] = *(const uint2*)(sc + ((st >> 1) & 1) * T::SCALES + row_of(r) * 16 + 8 * (st & 1));
+  };
+  const uint32_t pick = h ? 0x07050301u : 0x06040200u;
+  const auto sort_raw = [&](int r, Scl& c) {
+    c.v[r] = __builtin_amdgcn_perm(raw[r].y, raw[r].x, pick);
+  };
+  // one group of ops with `side(n)` issued after the n-th
+  const auto group = [&](auto sel, const Ops& o, const Scl& c, auto&& side) {
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int n = 0; n < TN; ++n) {
+        acc[m][n] = mma4_32<decltype(sel)::value>(o.v[m], c.v[m], o.v[TM + n], c.v[TM + n],
+                                                  acc[m][n]);
+        side(m * TN + n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
+  // of `count` things spread over a group's M slots, those of slot n
+  const auto spread = [](int n, int count, auto&& f) {
+#pragma unroll
+    for (int k = n * count / M; k < (n + 1) * count / M; ++k) f(k);
+  };
+  // of `count` things early in a group (the next group needs them), those of slot n
+  const auto early = [](int n, int count, auto&& f) {
+    constexpr int per_slot = (2 * NR + M - 1) / M;
+#pragma unroll
+    for (int k = n * per_slot; k < min(count, (n + 1) * per_slot); ++k) f(k);
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+
+  Ops f0, f1;
+  Scl cur;
+  // Step st, of parity k; MORE: at least two more steps follow, as the compiler
+  // may know.
+  const auto step = [&](auto kk, int st, auto more) {
+    constexpr int k = decltype(kk)::value;
+    constexpr bool MORE = decltype(more)::value;
+    const bool m1 = MORE || st + 1 < steps, m2 = MORE || st + 2 < steps;
+    group(I0{}, f0, cur, [&](int n) {
+      early(n, NR, [&](int r) { read_op(k, 1, nth(r), f1); });
+      if (m1) spread(n, T::J / 2, [&](int j) { copy(st + 1, T::J / 2 + j); });
+    });
+    group(I1{}, f1, cur, [&](int n) {
+      early(n, NR, [&](int r) { read_op(k, 2, nth(r), f0); });
+      if (m1) spread(n, NR, [&](int r) { read_raw(st + 1, r); });
+    });
+    group(I2{}, f0, cur, [&](int n) {
+      early(n, NR, [&](int r) { read_op(k, 3, nth(r), f1); });
+    });
+    if (m1) {
+      wait_copies();
+      __syncthreads();  // step st + 1 is there, and every wave holds the rest of st
+      if (st + 2 == steps && rem < 8) {
+        clear_tail();
+        __syncthreads();
+      }
+      // The scales of the turn after st + 1's, loaded a turn ago: ahead of the
+      // copies, because the compiler's wait for those loads waits for all.
+      if (k == 1 && (st >> 1) + 2 < turns) {
+        store_scales((st >> 1) + 2);
+        if ((st >> 1) + 3 < turns) load_scales((st >> 1) + 3);
+      }
+    }
+    group(I3{}, f1, cur, [&](int n) {
+      if (m1) early(n, NR, [&](int r) { read_op(k + 1, 0, nth(r), f0); });
+      if (m2) spread(n, T::J / 2, [&](int j) { copy(st + 2, j); });
+    });
+    if (m1) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) sort_raw(r, cur);
+    }
+  };
+
+#pragma unroll
+  for (int j = 0; j < T::J; ++j) copy(0, j);
+  load_scales(0);
+  store_scales(0);
+  if (turns > 1) {
+    load_scales(1);
+    store_scales(1);
+  }
+  if (turns > 2) load_scales(2);
+  wait_copies();
+  __syncthreads();
+  if (steps == 1 && rem < 8) {
+    clear_tail();
+    __syncthreads();
+  }
+  if (steps > 1) {
+#pragma unroll
+    for (int j = 0; j < T::J / 2; ++j) copy(1, j);
+  }
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    read_op(0, 0, r, f0);
+    read_raw(0, r);
+  }
+#pragma unroll
+  for (int r = 0; r < NR; ++r) sort_raw(r, cur);
+  int st = 0;
+#pragma unroll 1
+  for (; st + 3 < steps; st += 2) {
+    step(I0{}, st, std::true_type{});
+    step(I1{}, st + 1, std::true_type{});
+  }
+  step(I0{}, st, std::false_type{});
+  if (st + 1 < steps) step(I1{}, st + 1, std::false_type{});
+  if (st + 2 < steps) step(I0{}, st + 2, std::false_type{});
+
+  // The sums leave through LDS, 32 rows of the wave's columns at a time, so
+  // that a lane stores 16 bytes of one row.  Register 4 a + b of a 32 x 32 block
+  // is row 8 a + 4 h + b, column i; rows lie 8 words more than a multiple of 64
+  // apart, which puts the two halves' rows on different banks.
+  __syncthreads();  // every wave has read its last operands
+  constexpr int COLS = 32 * TN, PITCH = COLS + 8;
+  static_assert(T::NW * 32 * PITCH * 4 <= T::LDS, "");
+  float* const out = (float*)smem + wave * 32 * PITCH;
+  constexpr int E = YBF ? 8 : 4;  // values in 16 bytes
+  const bool wide = P.N % E == 0;
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        out[(8 * (j >> 2) + 4 * h + (j & 3)) * PITCH + 32 * n + i] = acc[m][n][j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the region is this wave's own
+    const int row0 = r0 + wm + 32 * m, col0 = n0 + wn;
+    if (wide) {
+      constexpr int LR = COLS / E;  // lanes to a row, a power of two
+#pragma unroll
+      for (int z = 0; z < 32 * LR / 64; ++z) {
+        const int row = (z * 64 + lane) / LR, col = (lane % LR) * E;
+        if (row0 + row < P.R && col0 + col < P.N) {
+          const size_t at = (size_t)(row0 + row) * P.N + col0 + col;
+          const float4* p = (const float4*)(out + row * PITCH + col);
+          if constexpr (YBF) {
+            const float4 u = p[0], v = p[1];
+            *(uint4*)((uint16_t*)P.y + at) = make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w),
+                                                        pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+          } else {
+            *(float4*)((float*)P.y + at) = p[0];
+          }
+        }
+      }
+    } else {
+      for (int o = lane; o < 32 * COLS; o += 64) {
+        const int row = o / COLS, col = o % COLS;
+        if (row0 + row < P.R && col0 + col < P.N) {
+          const size_t at = (size_t)(row0 + row) * P.N + col0 + col;
+          const float v = out[row * PITCH + col];
+          if constexpr (YBF) ((uint16_t*)P.y)[at] = (uint16_t)f32_to_bf16_bits(v);
+          else ((float*)P.y)[at] = v;
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+template <class T>
+static int launch_tile(const Mx4Params& P, bool ybf, hipStream_t s) {
+  const int tm = (P.R + T::BM - 1) / T::BM, tn = (P.N + T::BN - 1) / T::BN;
+  if ((long long)tm * tn > 0x7FFFFFFF)
+    return fail(QMOE_ERR_UNSUPPORTED, "qgemm_mxfp4_mxfp4: too many tiles");
+  const dim3 grid((unsigned)(tm * tn));
+  (void)hipFuncSetAttribute(ybf ? (const void*)mxfp4_tile_kernel<T, true>
+                                : (const void*)mxfp4_tile_kernel<T, false>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)T::LDS);
+  if (ybf)
+    return QMOE_LAUNCH("mxfp4_tile", (mxfp4_tile_kernel<T, true>), grid, T::THREADS, T::LDS, s, P,
+                       tm, tn);
+  return QMOE_LAUNCH("mxfp4_tile", (mxfp4_tile_kernel<T, false>), grid, T::THREADS, T::LDS, s, P,
+                     tm, tn);
+}
+
 }  // namespace qmoe
 
 using namespace qmoe;
@@ -173,6 +521,7 @@ extern "C" int qgemm_mxfp4_mxfp4(const void* W, int N, int K, const uint8_t* cod
   hipStream_t s = (hipStream_t)stream;
   if ((R + 63) / 64 > 65535)
     return fail(QMOE_ERR_UNSUPPORTED, "qgemm_mxfp4_mxfp4: R=%d too large", R);
+  if (R > 256) return launch_tile<Tile<2, 2, 4, 4>>(P, ybf, s);
   if (R <= 16) return launch_rows<1>(P, ybf, s);
   if (R <= 32) return launch_rows<2>(P, ybf, s);
   return launch_rows<4>(P, ybf, s);

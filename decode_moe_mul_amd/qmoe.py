@@ -471,55 +471,95 @@ def gemm_mxfp4_mxfp8(W, N, K, codes, scales, out=None):
 
 # ---------------------------------------------------- 4-bit activations --
 
+# These calls take a few microseconds on the GPU for a decode row, so their host
+# side is kept short: one test per tensor, pointers as plain ints, the raw
+# stream handle.
+
 ACT_FORMATS = ("q8", "mxfp8", "mxfp4")
+_ACT_TYPES = None   # format -> (values per code, code type, scale type)
 
 
-def _same_device(*ts):
-    """The one GPU that all the given tensors (None skipped) live on."""
-    ts = [t for t in ts if t is not None]
-    for t in ts:
-        _need(t.is_cuda, "tensors must be CUDA tensors")
-    dev = ts[0].device
-    _need(all(t.device == dev for t in ts), "tensors must be on one device")
-    return dev
+def _act_types():
+    global _ACT_TYPES
+    if _ACT_TYPES is None:
+        torch = _torch()
+        _ACT_TYPES = {"q8": (1, torch.int8, torch.float32), "mxfp8": (1, torch.uint8, torch.uint8),
+                      "mxfp4": (2, torch.uint8, torch.uint8)}
+    return _ACT_TYPES
 
 
-def _launch(name, dev, *args):
-    """Call entry point `name` with its device current, on that device's
-    current stream."""
+def _launch(name, index, *args):
+    """Call entry point `name` with GPU `index` current, on that GPU's current
+    stream."""
     torch = _torch()
-    if dev.index == torch.cuda.current_device():
-        _check(getattr(lib(), name)(*args, _stream()), name)
+    fn = getattr(_lib or lib(), name)
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            _check(getattr(lib(), name)(*args, _stream()), name)
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _check(st, name)
 
 
-def _out_dtype(dtype):
+def _gpu(t, what):
+    """The GPU index of a contiguous tensor."""
+    _need(t.is_cuda and t.is_contiguous(), f"{what} must be a contiguous CUDA tensor")
+    return t.get_device()
+
+
+def _require(t, shape, dtype, index, what):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        raise QmoeError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                        f"GPU {index}")
+
+
+def _float_code(dtype, what):
     torch = _torch()
-    _need(dtype in (torch.float32, torch.bfloat16), f"outputs are float32 or bfloat16, not {dtype}")
-    return F32 if dtype == torch.float32 else BF16
+    if dtype is torch.float32:
+        return F32
+    if dtype is torch.bfloat16:
+        return BF16
+    raise QmoeError(f"{what} must be float32 or bfloat16, not {dtype}")
 
 
-def _matrix(t, shape, dtype, what):
-    _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.is_contiguous(),
-          f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-
-
-def _act_out(fmt, R, K, dev, out):
-    """(codes, scales) tensors of activation format `fmt` for [R, K]."""
-    torch = _torch()
-    _need(fmt in ACT_FORMATS, f"activation format {fmt!r} is not one of {ACT_FORMATS}")
-    _need(K > 0 and K % 32 == 0, f"K={K} is not a multiple of 32")
-    kinds = {"q8": (K, torch.int8, torch.float32), "mxfp8": (K, torch.uint8, torch.uint8),
-             "mxfp4": (K // 2, torch.uint8, torch.uint8)}
-    width, ct, st = kinds[fmt]
+def _float_out(out, dtype, like, shape, index):
+    """(out, dtype code): a new tensor unless out is given."""
     if out is None:
-        return (torch.empty((R, width), dtype=ct, device=dev),
-                torch.empty((R, K // 32), dtype=st, device=dev))
-    _matrix(out[0], (R, width), ct, "codes")
-    _matrix(out[1], (R, K // 32), st, "scales")
+        dtype = _torch().float32 if dtype is None else dtype
+        code = _float_code(dtype, "outputs")
+        return like.new_empty(shape, dtype=dtype), code
+    code = _float_code(out.dtype, "outputs")
+    _require(out, shape, out.dtype if dtype is None else dtype, index, "out")
+    return out, code
+
+
+def _act_out(fmt, like, R, K, index, out):
+    """(codes, scales) of activation format `fmt` for [R, K]."""
+    kinds = _act_types().get(fmt)
+    if kinds is None:
+        raise QmoeError(f"activation format {fmt!r} is not one of {ACT_FORMATS}")
+    if K <= 0 or K % 32:
+        raise QmoeError(f"K={K} is not a multiple of 32")
+    per, ct, st = kinds
+    if out is None:
+        return like.new_empty((R, K // per), dtype=ct), like.new_empty((R, K // 32), dtype=st)
+    _require(out[0], (R, K // per), ct, index, "codes")
+    _require(out[1], (R, K // 32), st, index, "scales")
     return out
+
+
+def _act_in(codes, scales):
+    """(R, K, GPU index) of MXFP4 activations."""
+    torch = _torch()
+    _need(codes.dim() == 2, "codes must be [R, K/2]")
+    R, K = codes.shape
+    K *= 2
+    index = _gpu(codes, "codes")
+    _require(codes, (R, K // 2), torch.uint8, index, "codes")
+    _require(scales, (R, K // 32), torch.uint8, index, "scales")
+    return R, K, index
 
 
 def quantize_act_mxfp4(x, out=None):
@@ -527,51 +567,40 @@ def quantize_act_mxfp4(x, out=None):
     (two E2M1 codes per byte, low nibble first) and scales [R, K/32] uint8
     (E8M0)."""
     _need(x.dim() == 2, "x must be [R, K]")
-    _cuda_contig(x)
     R, K = x.shape
-    codes, scales = _act_out("mxfp4", R, K, x.device, out)
-    dev = _same_device(x, codes, scales)
-    _launch("qquantize_act_mxfp4", dev, _p(x), _dtype_code(x), R, K, _p(codes), _p(scales))
+    index, xd = _gpu(x, "x"), _float_code(x.dtype, "activations")
+    codes, scales = _act_out("mxfp4", x, R, K, index, out)
+    _launch("qquantize_act_mxfp4", index, x.data_ptr(), xd, R, K, codes.data_ptr(),
+            scales.data_ptr())
     return codes, scales
 
 
 def dequantize_act_mxfp4(codes, scales, dtype=None, out=None):
     """The values [R, K] of MXFP4 activations (float32 unless dtype says
     bfloat16)."""
-    torch = _torch()
-    R, K = codes.shape[0], 2 * codes.shape[1]
-    _matrix(codes, (R, K // 2), torch.uint8, "codes")
-    _matrix(scales, (R, K // 32), torch.uint8, "scales")
-    if out is None:
-        dtype = torch.float32 if dtype is None else dtype
-        _out_dtype(dtype)
-        out = torch.empty((R, K), dtype=dtype, device=codes.device)
-    else:
-        _matrix(out, (R, K), out.dtype if dtype is None else dtype, "out")
-    dev = _same_device(codes, scales, out)
-    _launch("qdequant_act_mxfp4", dev, _p(codes), _p(scales), R, K, _p(out),
-            _out_dtype(out.dtype))
+    R, K, index = _act_in(codes, scales)
+    out, yd = _float_out(out, dtype, codes, (R, K), index)
+    _launch("qdequant_act_mxfp4", index, codes.data_ptr(), scales.data_ptr(), R, K,
+            out.data_ptr(), yd)
     return out
 
 
 def _norm_args(x, w, eps, res, res_out):
-    torch = _torch()
     _need(x.dim() == 2, "x must be [R, K]")
     R, K = x.shape
-    _cuda_contig(x, w, res, res_out)
-    _matrix(w, (K,), torch.float32, "w")
-    code = 0
-    if res is not None:
-        code = _dtype_code(res)
-        _matrix(res, (R, K), res.dtype, "res")
-        if res_out is None:
-            res_out = torch.empty_like(res)
-        _matrix(res_out, (R, K), res.dtype, "res_out")
-    else:
+    index, xd = _gpu(x, "x"), _float_code(x.dtype, "activations")
+    _require(w, (K,), _torch().float32, index, "w")
+    if res is None:
         _need(res_out is None, "res_out without res")
-    dev = _same_device(x, w, res, res_out)
-    args = (_p(x), _dtype_code(x), _p(res), _p(res_out), code, _p(w), float(eps), R, K)
-    return dev, R, K, res_out, args
+        return index, R, K, None, (x.data_ptr(), xd, None, None, 0, w.data_ptr(), eps, R, K)
+    rd = _float_code(res.dtype, "res")
+    _require(res, (R, K), res.dtype, index, "res")
+    if res_out is None:
+        res_out = _torch().empty_like(res)
+    elif res_out is not res:
+        _require(res_out, (R, K), res.dtype, index, "res_out")
+    return index, R, K, res_out, (x.data_ptr(), xd, res.data_ptr(), res_out.data_ptr(), rd,
+                                  w.data_ptr(), eps, R, K)
 
 
 def norm(x, w, eps, res=None, res_out=None, dtype=None, out=None):
@@ -579,26 +608,18 @@ def norm(x, w, eps, res=None, res_out=None, dtype=None, out=None):
     sqrt(mean(h^2) + eps) in float32, or dtype.  Returns y, with res (y, h);
     h has res' type and goes to res_out (a new tensor unless given; res itself
     for an update in place)."""
-    torch = _torch()
-    dev, R, K, h, args = _norm_args(x, w, eps, res, res_out)
-    if out is None:
-        dtype = torch.float32 if dtype is None else dtype
-        _out_dtype(dtype)
-        out = torch.empty((R, K), dtype=dtype, device=dev)
-    else:
-        _matrix(out, (R, K), out.dtype if dtype is None else dtype, "out")
-        _same_device(x, out)
-    _launch("qnorm", dev, *args, _p(out), _out_dtype(out.dtype))
+    index, R, K, h, args = _norm_args(x, w, eps, res, res_out)
+    out, yd = _float_out(out, dtype, x, (R, K), index)
+    _launch("qnorm", index, *args, out.data_ptr(), yd)
     return out if res is None else (out, h)
 
 
 def norm_act(fmt, x, w, eps, res=None, res_out=None, out=None):
     """norm's float32 rows in activation format fmt ("q8", "mxfp8", "mxfp4"):
     (codes, scales), with res (codes, scales, h)."""
-    dev, R, K, h, args = _norm_args(x, w, eps, res, res_out)
-    codes, scales = _act_out(fmt, R, K, dev, out)
-    _same_device(x, codes, scales)
-    _launch(f"qnorm_act_{fmt}", dev, *args, _p(codes), _p(scales))
+    index, R, K, h, args = _norm_args(x, w, eps, res, res_out)
+    codes, scales = _act_out(fmt, x, R, K, index, out)
+    _launch("qnorm_act_" + fmt, index, *args, codes.data_ptr(), scales.data_ptr())
     return (codes, scales) if res is None else (codes, scales, h)
 
 
@@ -606,42 +627,35 @@ def swiglu_act(fmt, gate, up, out=None):
     """gate / (1 + exp(-gate)) * up [R, K] in activation format fmt: (codes,
     scales).  gate and up are float32 or bfloat16, with contiguous rows; the
     rows may lie further apart (the two halves of one [R, 2K] tensor)."""
-    _need(gate.dim() == 2 and gate.shape == up.shape and gate.dtype == up.dtype,
-          "gate and up must be [R, K] of one type")
+    _need(gate.dim() == 2 and gate.is_cuda and gate.shape == up.shape and gate.dtype is up.dtype
+          and gate.get_device() == up.get_device(),
+          "gate and up must be CUDA tensors [R, K] of one type on one GPU")
     R, K = gate.shape
-    dev = _same_device(gate, up)
+    index, xd = gate.get_device(), _float_code(gate.dtype, "gate and up")
     ld = K
-    if R > 1:
-        ld = gate.stride(0)
-        _need(gate.stride(1) == up.stride(1) == 1 and up.stride(0) == ld,
+    if R > 0:
+        (ld, one), (ld_up, one_up) = gate.stride(), up.stride()
+        if R == 1:
+            ld = ld_up = K   # the distance of a single row says nothing
+        _need(one == one_up == 1 and ld == ld_up,
               "gate and up must have contiguous rows, equally far apart")
-    else:
-        _need(R == 0 or gate.stride(1) == up.stride(1) == 1, "gate and up must have contiguous rows")
-    codes, scales = _act_out(fmt, R, K, dev, out)
-    _same_device(gate, codes, scales)
-    _launch(f"qswiglu_act_{fmt}", dev, _p(gate), _p(up), _dtype_code(gate), ld, R, K, _p(codes),
-            _p(scales))
+    codes, scales = _act_out(fmt, gate, R, K, index, out)
+    _launch("qswiglu_act_" + fmt, index, gate.data_ptr(), up.data_ptr(), xd, ld, R, K,
+            codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def gemm_mxfp4_mxfp4(W, N, K, codes, scales, dtype=None, out=None):
     """y [R, N] (float32 unless dtype says bfloat16) = W (MXFP4 [N, K]) times
     the MXFP4 activations; R from one decode row to a prefill chunk."""
-    torch = _torch()
-    R = codes.shape[0]
-    _matrix(codes, (R, K // 2), torch.uint8, "codes")
-    _matrix(scales, (R, K // 32), torch.uint8, "scales")
-    _need(W.dtype == torch.uint8 and W.is_contiguous() and W.numel() >= tensor_bytes("mxfp4", N, K),
-          "W must be a packed MXFP4 [N, K] tensor")
-    if out is None:
-        dtype = torch.float32 if dtype is None else dtype
-        _out_dtype(dtype)
-        out = torch.empty((R, N), dtype=dtype, device=codes.device)
-    else:
-        _matrix(out, (R, N), out.dtype if dtype is None else dtype, "out")
-    dev = _same_device(W, codes, scales, out)
-    _launch("qgemm_mxfp4_mxfp4", dev, _p(W), N, K, _p(codes), _p(scales), R, _p(out),
-            _out_dtype(out.dtype))
+    R, K2, index = _act_in(codes, scales)
+    _need(K2 == K, f"the activations have {K2} values a row, the weights {K}")
+    _need(N >= 0 and W.dtype is codes.dtype and W.get_device() == index and W.is_contiguous()
+          and W.numel() >= -(-N * K // 512) * 256 + -(-N * K // 8192) * 256,
+          "W must be a packed MXFP4 [N, K] tensor on the activations' GPU")
+    out, yd = _float_out(out, dtype, codes, (R, N), index)
+    _launch("qgemm_mxfp4_mxfp4", index, W.data_ptr(), N, K, codes.data_ptr(), scales.data_ptr(),
+            R, out.data_ptr(), yd)
     return out
 
 
