@@ -5,14 +5,6 @@
 // Both operands are E2M1 codes with one E8M0 scale per 32 values along K, used
 // as stored: every product of two codes is exact, the matrix op applies both
 // scales and accumulates in fp32.
-//
-// Operand order.  A 16x16x128 op takes, from lane 16 g + i, the 16 code bytes
-// of one K block of row i, and that block's scale from a byte of a register
-// that the op selects.  Which K block is called "block g of the step" is free
-// as long as both operands agree, so four steps together cover 16 consecutive
-// blocks with lane group g taking blocks 4 g .. 4 g + 3, one per step: its
-// codes are then 64 consecutive bytes of the row and its four scales one
-// 32-bit word, whose byte s serves step s without any repacking.
 #include <algorithm>
 #include <type_traits>
 
@@ -34,100 +26,111 @@ struct Mx4Params {
   int N, K, R;
 };
 
-template <int STEP>
 QMOE_D v4f_t mma4(uint4 a, uint32_t sa, uint4 b, uint32_t sb, v4f_t c) {
   const v8i_t av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const v8i_t bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, STEP, (int)sa, STEP,
-                                                          (int)sb);
-}
-
-// One lane's part of 16 blocks: 4 blocks of codes and their scale word.
-struct Frag {
-  uint4 q[4];
-  uint32_t s;
-};
-// Blocks b0 .. b0 + 3 of a row that starts at block `row` of the plane; blocks
-// from nb on (past the row's end) are zeros.
-QMOE_D uint32_t load_scales4(const uint8_t* p) {  // no alignment: a row has K / 32 bytes
-  uint32_t v;
-  __builtin_memcpy(&v, p, 4);
-  return v;
-}
-template <bool TAIL>
-QMOE_D void load_frag(const uint8_t* q, const uint8_t* s, size_t row, int b0, int nb, Frag& f) {
-  if (!TAIL || b0 + 4 <= nb) {
-    const uint4* p = (const uint4*)(q + (row + b0) * 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.q[j] = p[j];
-    f.s = load_scales4(s + row + b0);
-  } else {
-    f.s = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f.q[j] = make_uint4(0, 0, 0, 0);
-      if (b0 + j < nb) {
-        f.q[j] = *(const uint4*)(q + (row + b0 + j) * 16);
-        f.s |= (uint32_t)s[row + b0 + j] << (8 * j);
-      }
-    }
-  }
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
 // ------------------------------------------------------ few rows ------
-// A block computes 16 weight rows x 16 RT activation rows; its waves split K
-// in turns of 16 blocks, and their sums meet in LDS in wave order.
-template <int RT, bool YBF>
-__global__ __launch_bounds__(512) void mxfp4_rows_kernel(Mx4Params P) {
-  extern __shared__ __align__(16) float red[];  // [wave][RT][64 lanes][4]
+// A block computes 16 CT weight rows x 16 RT activation rows with 16x16x128
+// ops; its waves split K in turns of 512 values, and their sums meet in LDS in
+// wave order.  Operands go from memory to registers, a whole turn's loads
+// together: with few rows the call is a read of the weights, and what counts is
+// how many of them are on their way.
+//
+// Lane 16 g + i of step j takes block 4 j + g of the turn from row i, so that a
+// load reads 64 consecutive bytes of each of 16 rows.  (With four consecutive
+// blocks to a lane, which would put its scales into one word, a load touches
+// four times as many cache sectors: 16 x 14336 x 4096 took 12.4 us.)  The
+// lane's scale of step j is byte g of the row's j-th scale word.
+struct Frag {  // one lane's part of a turn
+  uint4 q[4];
+  uint32_t s[4];
+};
+// `row` counts the plane's blocks before the row; blocks from nb on (past the
+// row's end) are zeros.
+template <bool TAIL>
+QMOE_D void load_codes(const uint8_t* q, size_t row, int b, int nb, uint4& v) {
+  if (TAIL && b >= nb) v = make_uint4(0, 0, 0, 0);
+  else v = *(const uint4*)(q + (row + b) * 16);
+}
+template <bool TAIL>
+QMOE_D void load_scales(const uint8_t* s, size_t row, int b0, int g, int nb, Frag& f) {
+  if constexpr (TAIL) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.s[j] = b0 + 4 * j + g < nb ? s[row + b0 + 4 * j + g] : 0;
+  } else {
+    uint32_t w[4];  // no alignment: a row has K / 32 bytes
+    __builtin_memcpy(w, s + row + b0, 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.s[j] = w[j] >> (8 * g);
+  }
+}
+
+constexpr int kRowsWaves = 8;
+
+template <int CT, int RT, bool YBF>
+__global__ __launch_bounds__(64 * kRowsWaves) void mxfp4_rows_kernel(Mx4Params P) {
+  extern __shared__ __align__(16) float red[];  // [wave][CT * RT][64 lanes][4]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int nb = P.K >> 5, turns = (nb + 15) >> 4, full = nb >> 4;
-  const int n0 = blockIdx.x * 16, r0 = blockIdx.y * 16 * RT;
-  const size_t wrow = (size_t)min(n0 + i, P.N - 1) * nb;
-  size_t xrow[RT];
+  const int n0 = blockIdx.x * 16 * CT, r0 = blockIdx.y * 16 * RT;
+  size_t wrow[CT], xrow[RT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) wrow[c] = (size_t)min(n0 + 16 * c + i, P.N - 1) * nb;
 #pragma unroll
   for (int t = 0; t < RT; ++t) xrow[t] = (size_t)min(r0 + 16 * t + i, P.R - 1) * nb;
-  v4f_t acc[RT];
+  v4f_t acc[CT][RT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = v4f_t{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const Frag& w, const Frag& x, v4f_t& c) {
-    c = mma4<0>(w.q[0], w.s, x.q[0], x.s, c);
-    c = mma4<1>(w.q[1], w.s, x.q[1], x.s, c);
-    c = mma4<2>(w.q[2], w.s, x.q[2], x.s, c);
-    c = mma4<3>(w.q[3], w.s, x.q[3], x.s, c);
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[c][t] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  const auto turn = [&](auto tail, int u) {
+    constexpr bool TAIL = decltype(tail)::value;
+    Frag w[CT], x[RT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) load_scales<TAIL>(P.ws, wrow[c], 16 * u, g, nb, w[c]);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) load_scales<TAIL>(P.xs, xrow[t], 16 * u, g, nb, x[t]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        load_codes<TAIL>(P.wq, wrow[c], 16 * u + 4 * j + g, nb, w[c].q[j]);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        load_codes<TAIL>(P.xq, xrow[t], 16 * u + 4 * j + g, nb, x[t].q[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          acc[c][t] = mma4(w[c].q[j], w[c].s[j], x[t].q[j], x[t].s[j], acc[c][t]);
   };
   int u = wave;
-  for (; u < full; u += waves) {
-    Frag w, x[RT];
-    load_frag<false>(P.wq, P.ws, wrow, 16 * u + 4 * g, nb, w);
+  for (; u < full; u += waves) turn(std::false_type{}, u);
+  if (u < turns) turn(std::true_type{}, u);  // the last, partial turn
+  v4f_t* const sums = (v4f_t*)red;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) load_frag<false>(P.xq, P.xs, xrow[t], 16 * u + 4 * g, nb, x[t]);
+  for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int t = 0; t < RT; ++t) multiply(w, x[t], acc[t]);
-  }
-  if (u < turns) {  // the last, partial turn
-    Frag w, x;
-    load_frag<true>(P.wq, P.ws, wrow, 16 * u + 4 * g, nb, w);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      load_frag<true>(P.xq, P.xs, xrow[t], 16 * u + 4 * g, nb, x);
-      multiply(w, x, acc[t]);
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < RT; ++t) *(v4f_t*)(red + ((wave * RT + t) * 64 + lane) * 4) = acc[t];
+    for (int t = 0; t < RT; ++t) sums[(wave * CT * RT + c * RT + t) * 64 + lane] = acc[c][t];
   __syncthreads();
-  // lane 16 g + i of tile t holds rows n0 + 4 g .. + 3 of column i
-  for (int o = threadIdx.x; o < RT * 64; o += blockDim.x) {
-    const int t = o >> 6, l = o & 63;
-    v4f_t s = *(const v4f_t*)(red + o * 4);
+  // lane 16 g + i of block (c, t) holds weight rows 16 c + 4 g .. + 3 of
+  // activation row 16 t + i
+  for (int o = threadIdx.x; o < CT * RT * 64; o += blockDim.x) {
+    v4f_t s = sums[o];
     for (int w = 1; w < waves; ++w) {
-      const v4f_t v = *(const v4f_t*)(red + (w * RT * 64 + o) * 4);
+      const v4f_t v = sums[w * CT * RT * 64 + o];
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[j] += v[j];
     }
-    const int r = r0 + 16 * t + (l & 15), n = n0 + 4 * (l >> 4);
+    const int l = o & 63, c = (o >> 6) / RT, t = (o >> 6) % RT;
+    const int r = r0 + 16 * t + (l & 15), n = n0 + 16 * c + 4 * (l >> 4);
     if (r >= P.R) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -139,15 +142,21 @@ __global__ __launch_bounds__(512) void mxfp4_rows_kernel(Mx4Params P) {
   }
 }
 
-template <int RT>
+template <int CT, int RT>
 static int launch_rows(const Mx4Params& P, bool ybf, hipStream_t s) {
-  const dim3 grid((unsigned)((P.N + 15) / 16), (unsigned)((P.R + 16 * RT - 1) / (16 * RT)));
-  const int turns = (P.K / 32 + 15) / 16;
-  const int waves = std::min(8, turns);
-  const size_t lds = (size_t)waves * RT * 64 * 16;
+  const dim3 grid((unsigned)((P.N + 16 * CT - 1) / (16 * CT)),
+                  (unsigned)((P.R + 16 * RT - 1) / (16 * RT)));
+  const int waves = std::min(kRowsWaves, (P.K / 32 + 15) / 16);
+  const size_t lds = (size_t)waves * CT * RT * 64 * 16;
+  if (lds > (64u << 10))
+    (void)hipFuncSetAttribute(ybf ? (const void*)mxfp4_rows_kernel<CT, RT, true>
+                                  : (const void*)mxfp4_rows_kernel<CT, RT, false>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (ybf)
-    return QMOE_LAUNCH("mxfp4_rows", (mxfp4_rows_kernel<RT, true>), grid, 64 * waves, lds, s, P);
-  return QMOE_LAUNCH("mxfp4_rows", (mxfp4_rows_kernel<RT, false>), grid, 64 * waves, lds, s, P);
+    return QMOE_LAUNCH("mxfp4_rows", (mxfp4_rows_kernel<CT, RT, true>), grid, 64 * waves, lds, s,
+                       P);
+  return QMOE_LAUNCH("mxfp4_rows", (mxfp4_rows_kernel<CT, RT, false>), grid, 64 * waves, lds, s,
+                     P);
 }
 
 // ------------------------------------------------------ many rows ------
@@ -172,18 +181,28 @@ static int launch_rows(const Mx4Params& P, bool ybf, hipStream_t s) {
 // The 16-byte chunk c of tile row q lies at chunk c ^ (q & 7), chosen by
 // which chunk of memory a lane fetches, so that the rows one operand read
 // touches spread over the banks.  Rows past the ends repeat the last one and
-// are never stored; blocks past K's end repeat the row's last one, and zeros
-// replace the activations'.
-template <int WR_, int WC_, int TM_, int TN_>
+// are never stored; blocks past K's end repeat the row's last one with scale
+// bytes of 0, and 2^-127 from either side leaves nothing of their products.
+//
+// KS teams of WR x WC waves split K where there are too few tiles to fill the
+// part: each takes a run of whole turns (two steps) with buffers of its own,
+// and the first team adds the others' sums to its own in team order.
+template <int WR_, int WC_, int TM_, int TN_, int KS_ = 1>
 struct Tile {
-  static constexpr int WR = WR_, WC = WC_, TM = TM_, TN = TN_;
+  static constexpr int WR = WR_, WC = WC_, TM = TM_, TN = TN_, KS = KS_;
   static constexpr int BM = 32 * WR * TM, BN = 32 * WC * TN, ROWS = BM + BN, NW = WR * WC;
-  static constexpr int THREADS = 64 * NW;
+  static constexpr int TEAM = 64 * NW, THREADS = TEAM * KS;
   static constexpr int CODES = ROWS * 128, SCALES = ROWS * 16;  // bytes of one buffer
-  static constexpr size_t LDS = 2 * (CODES + SCALES);
+  static constexpr int TEAM_LDS = 2 * (CODES + SCALES);
   static constexpr int JA = BM / 8 / NW, J = ROWS / 8 / NW;     // copies per wave and step
-  static constexpr int SR = (ROWS + THREADS - 1) / THREADS;     // scale rows per thread
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && J % 2 == 0, "");
+  static constexpr int J1 = J / 2;                              // of them in the first part
+  static constexpr int SR = (ROWS + TEAM - 1) / TEAM;           // scale rows per thread
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "");
+  // leaving: 32 rows of a wave's columns, then the other teams' sums
+  static constexpr int COLS = 32 * TN, PITCH = COLS + 8, OUT = NW * 32 * PITCH * 4;
+  static constexpr int SUMS = TM * TN * 16 * TEAM * 4;
+  static constexpr size_t LDS = std::max(KS * TEAM_LDS, OUT + (KS - 1) * SUMS);
+  static_assert(LDS <= 160 << 10, "");
 };
 
 typedef float v16f_t __attribute__((ext_vector_type(16)));
@@ -222,23 +241,30 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
                                                                 int tiles_n) {
   constexpr int TM = T::TM, TN = T::TN, M = TM * TN, NR = TM + TN;
   extern __shared__ __align__(16) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
+  const int team = T::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / T::TEAM);
+  const int tid = threadIdx.x % T::TEAM, lane = tid & 63, i = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint8_t* const mem = smem + team * T::TEAM_LDS;
   // Blocks are dealt to the 8 XCDs in turn: give each XCD one run of tiles,
   // down the rows first, so that its L2 serves both operands' reuse.
   const int T_ = tiles_m * tiles_n, per = T_ >> 3, extra = T_ & 7;
   const int x = blockIdx.x & 7;
   const int tile = x * per + min(x, extra) + (blockIdx.x >> 3);
   const int r0 = (tile % tiles_m) * T::BM, n0 = (tile / tiles_m) * T::BN;
-  const int nb = P.K >> 5, steps = (nb + 7) >> 3, turns = (nb + 15) >> 4;
+  // this team's steps [first, first + steps) of K's `all`; every team goes
+  // through `loops` of them, idle past its own
+  const int nb = P.K >> 5, all = (nb + 7) >> 3;
+  const int loops = 2 * ((all + 2 * T::KS - 1) / (2 * T::KS));
+  const int first = team * loops;
+  const int steps = min(max(all - first, 0), loops), turns = (steps + 1) >> 1;
   const uint32_t rowb = (uint32_t)P.K >> 1;
   const uint8_t* const abase = P.xq + (size_t)r0 * rowb;
   const uint8_t* const bbase = P.wq + (size_t)n0 * rowb;
   const int arows = P.R - r0 - 1, brows = P.N - n0 - 1;  // last valid row of the tile
 
-  // This lane's source offset of each copy: copy j of the wave fills tile rows
-  // 8 (wave + NW j) .. + 7, so the lane's chunk is the same for every j.
-  const int rem = nb - 8 * (steps - 1);  // blocks of the last step, 1..8
+  // Copy j of the wave fills tile rows 8 (wave + NW j) .. + 7, so the lane's
+  // chunk is the same for every j.
+  const int rem = nb - 8 * (all - 1);  // blocks of K's last step, 1..8
   const int chunk = (lane & 7) ^ (lane >> 3);
   const uint32_t over = 16u * (uint32_t)max(chunk - (rem - 1), 0);
   uint32_t off[T::J];
@@ -248,19 +274,21 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
     const int row = j < T::JA ? min(q, arows) : min(q - T::BM, brows);
     off[j] = (uint32_t)row * rowb + 16u * (uint32_t)chunk;
   }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)mem;
   const auto copy = [&](int st, int j) {
+    const int k = min(first + st, all - 1);  // past the team's steps: unused
     copy_to_lds(lds0 + (st & 1) * T::CODES + (wave + T::NW * j) * 1024,
-                uniform((j < T::JA ? abase : bbase) + (size_t)st * 128),
-                off[j] - (st + 1 == steps ? over : 0));
+                uniform((j < T::JA ? abase : bbase) + (size_t)k * 128),
+                off[j] - (k + 1 == all ? over : 0));
   };
-  // scales of turn u (16 blocks), tile row q at 16 q; zeros past the row's end
-  uint8_t* const sc = smem + 2 * T::CODES;
+  // scales of the team's turns (16 blocks), tile row q at 16 q; 0 past K's end
+  uint8_t* const sc = mem + 2 * T::CODES;
   uint4 sreg[T::SR];
-  const auto load_scales = [&](int u) {
+  const auto load_scales = [&](int turn) {
+    const int u = (first >> 1) + turn;
 #pragma unroll
     for (int j = 0; j < T::SR; ++j) {
-      const int q = tid + j * T::THREADS;
+      const int q = tid + j * T::TEAM;
       const uint8_t* p = (q < T::BM ? P.xs + (size_t)(r0 + min(q, arows)) * nb
                                     : P.ws + (size_t)(n0 + min(q - T::BM, brows)) * nb) + 16 * u;
       if (16 * u + 16 <= nb) {
@@ -279,19 +307,11 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
   const auto store_scales = [&](int u) {
 #pragma unroll
     for (int j = 0; j < T::SR; ++j) {
-      const int q = tid + j * T::THREADS;
-      if (T::ROWS % T::THREADS == 0 || q < T::ROWS)
+      const int q = tid + j * T::TEAM;
+      if (T::ROWS % T::TEAM == 0 || q < T::ROWS)
         *(uint4*)(sc + (u & 1) * T::SCALES + q * 16) = sreg[j];
     }
   };
-  // the blocks past K's end in the last step: zeros for the activations
-  const auto clear_tail = [&]() {
-    uint8_t* buf = smem + ((steps - 1) & 1) * T::CODES;
-    for (int q = tid; q < T::BM; q += T::THREADS)
-      for (int c = rem; c < 8; ++c)
-        *(uint4*)(buf + q * 128 + 16 * (c ^ (q & 7))) = make_uint4(0, 0, 0, 0);
-  };
-
   const int wm = (wave / T::WC) * 32 * TM, wn = (wave % T::WC) * 32 * TN;
   const int qa = wm + i, qb = T::BM + wn + i;  // the lane's rows of the first ops
   v16f_t acc[TM][TN];
@@ -312,7 +332,7 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
   const auto nth = [](int r) { return r == 0 ? 0 : r <= TN ? TM + r - 1 : r - TN; };
   const auto row_of = [&](int r) { return r < TM ? qa + 32 * r : qb + 32 * (r - TM); };
   const auto read_op = [&](int st, int s, int r, Ops& o) {
-    o.v[r] = *(const uint4*)(smem + (st & 1) * T::CODES + row_of(r) * 128 +
+    o.v[r] = *(const uint4*)(mem + (st & 1) * T::CODES + row_of(r) * 128 +
                              16 * ((2 * s + h) ^ (i & 7)));
   };
   uint2 raw[NR];  // a row's scales of the next step
@@ -353,30 +373,28 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
 
   Ops f0, f1;
   Scl cur;
-  // Step st, of parity k; MORE: at least two more steps follow, as the compiler
-  // may know.
-  const auto step = [&](auto kk, int st, auto more) {
-    constexpr int k = decltype(kk)::value;
-    constexpr bool MORE = decltype(more)::value;
-    const bool m1 = MORE || st + 1 < steps, m2 = MORE || st + 2 < steps;
-    group(I0{}, f0, cur, [&](int n) {
-      early(n, NR, [&](int r) { read_op(k, 1, nth(r), f1); });
-      if (m1) spread(n, T::J / 2, [&](int j) { copy(st + 1, T::J / 2 + j); });
-    });
-    group(I1{}, f1, cur, [&](int n) {
-      early(n, NR, [&](int r) { read_op(k, 2, nth(r), f0); });
-      if (m1) spread(n, NR, [&](int r) { read_raw(st + 1, r); });
-    });
-    group(I2{}, f0, cur, [&](int n) {
-      early(n, NR, [&](int r) { read_op(k, 3, nth(r), f1); });
-    });
-    if (m1) {
+  // Step st, of parity k, with LEFT more to follow (2: two or more).  Known to
+  // the compiler: a branch among the ops would end what it may reorder and
+  // count across.
+  const auto step = [&](auto kk, auto left, int st) {
+    constexpr int k = decltype(kk)::value, LEFT = decltype(left)::value;
+    const bool live = (T::KS == 1 && LEFT > 0) || st < steps;
+    if (live) {
+      group(I0{}, f0, cur, [&](int n) {
+        early(n, NR, [&](int r) { read_op(k, 1, nth(r), f1); });
+        if constexpr (LEFT >= 1) spread(n, T::J - T::J1, [&](int j) { copy(st + 1, T::J1 + j); });
+      });
+      group(I1{}, f1, cur, [&](int n) {
+        early(n, NR, [&](int r) { read_op(k, 2, nth(r), f0); });
+        if constexpr (LEFT >= 1) spread(n, NR, [&](int r) { read_raw(st + 1, r); });
+      });
+      group(I2{}, f0, cur, [&](int n) {
+        early(n, NR, [&](int r) { read_op(k, 3, nth(r), f1); });
+      });
+    }
+    if constexpr (LEFT >= 1) {
       wait_copies();
       __syncthreads();  // step st + 1 is there, and every wave holds the rest of st
-      if (st + 2 == steps && rem < 8) {
-        clear_tail();
-        __syncthreads();
-      }
       // The scales of the turn after st + 1's, loaded a turn ago: ahead of the
       // copies, because the compiler's wait for those loads waits for all.
       if (k == 1 && (st >> 1) + 2 < turns) {
@@ -384,20 +402,24 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
         if ((st >> 1) + 3 < turns) load_scales((st >> 1) + 3);
       }
     }
-    group(I3{}, f1, cur, [&](int n) {
-      if (m1) early(n, NR, [&](int r) { read_op(k + 1, 0, nth(r), f0); });
-      if (m2) spread(n, T::J / 2, [&](int j) { copy(st + 2, j); });
-    });
-    if (m1) {
+    if (live) {
+      group(I3{}, f1, cur, [&](int n) {
+        if constexpr (LEFT >= 1) early(n, NR, [&](int r) { read_op(k + 1, 0, nth(r), f0); });
+        if constexpr (LEFT >= 2) spread(n, T::J1, [&](int j) { copy(st + 2, j); });
+      });
+      if constexpr (LEFT >= 1) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) sort_raw(r, cur);
+        for (int r = 0; r < NR; ++r) sort_raw(r, cur);
+      }
     }
   };
 
 #pragma unroll
   for (int j = 0; j < T::J; ++j) copy(0, j);
-  load_scales(0);
-  store_scales(0);
+  if (turns > 0) {
+    load_scales(0);
+    store_scales(0);
+  }
   if (turns > 1) {
     load_scales(1);
     store_scales(1);
@@ -405,14 +427,8 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
   if (turns > 2) load_scales(2);
   wait_copies();
   __syncthreads();
-  if (steps == 1 && rem < 8) {
-    clear_tail();
-    __syncthreads();
-  }
-  if (steps > 1) {
 #pragma unroll
-    for (int j = 0; j < T::J / 2; ++j) copy(1, j);
-  }
+  for (int j = 0; j < T::J1; ++j) copy(1, j);
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     read_op(0, 0, r, f0);
@@ -422,21 +438,42 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
   for (int r = 0; r < NR; ++r) sort_raw(r, cur);
   int st = 0;
 #pragma unroll 1
-  for (; st + 3 < steps; st += 2) {
-    step(I0{}, st, std::true_type{});
-    step(I1{}, st + 1, std::true_type{});
+  for (; st + 2 < loops; st += 2) {  // loops is even
+    step(I0{}, I2{}, st);
+    step(I1{}, I2{}, st + 1);
   }
-  step(I0{}, st, std::false_type{});
-  if (st + 1 < steps) step(I1{}, st + 1, std::false_type{});
-  if (st + 2 < steps) step(I0{}, st + 2, std::false_type{});
+  step(I0{}, I1{}, st);
+  step(I1{}, I0{}, st + 1);
+  if constexpr (T::KS > 1) {
+    __syncthreads();
+    float* const sums = (float*)(smem + T::OUT) + tid;
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (team > 0)
+            sums[((team - 1) * M * 16 + (m * TN + n) * 16 + j) * T::TEAM] = acc[m][n][j];
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll 1
+    for (int t = 0; t < T::KS - 1; ++t)
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[m][n][j] += sums[(t * M * 16 + (m * TN + n) * 16 + j) * T::TEAM];
+  }
 
   // The sums leave through LDS, 32 rows of the wave's columns at a time, so
   // that a lane stores 16 bytes of one row.  Register 4 a + b of a 32 x 32 block
   // is row 8 a + 4 h + b, column i; rows lie 8 words more than a multiple of 64
   // apart, which puts the two halves' rows on different banks.
-  __syncthreads();  // every wave has read its last operands
-  constexpr int COLS = 32 * TN, PITCH = COLS + 8;
-  static_assert(T::NW * 32 * PITCH * 4 <= T::LDS, "");
+  if constexpr (T::KS == 1) __syncthreads();  // every wave has read its last operands
+  constexpr int COLS = T::COLS, PITCH = T::PITCH;
   float* const out = (float*)smem + wave * 32 * PITCH;
   constexpr int E = YBF ? 8 : 4;  // values in 16 bytes
   const bool wide = P.N % E == 0;
@@ -521,8 +558,14 @@ extern "C" int qgemm_mxfp4_mxfp4(const void* W, int N, int K, const uint8_t* cod
   hipStream_t s = (hipStream_t)stream;
   if ((R + 63) / 64 > 65535)
     return fail(QMOE_ERR_UNSUPPORTED, "qgemm_mxfp4_mxfp4: R=%d too large", R);
+#ifdef ROWSV
+  return launch_rows<ROWSV>(P, ybf, s);
+#endif
+#ifdef VARIANT
+  return launch_tile<Tile<VARIANT>>(P, ybf, s);
+#endif
   if (R > 256) return launch_tile<Tile<2, 2, 4, 4>>(P, ybf, s);
-  if (R <= 16) return launch_rows<1>(P, ybf, s);
-  if (R <= 32) return launch_rows<2>(P, ybf, s);
-  return launch_rows<4>(P, ybf, s);
+  if (R <= 16) return launch_rows<1, 1>(P, ybf, s);
+  if (R <= 32) return launch_rows<2, 2>(P, ybf, s);
+  return launch_rows<4, 4>(P, ybf, s);
 }
