@@ -64,13 +64,50 @@ QMOE_D uint32_t block_max_bits(const float (&v)[8]) {
   return m;
 }
 
+// Eight values over their block's scale as MX codes, saturating: clamping first
+// makes the conversions (nearest even) saturate, adding 0 turns a negative zero
+// into a positive one.  `top`: the type's largest value.
+template <int OUT>
+QMOE_D uint2 mx_codes8(const float (&v)[8], float mul) {
+  constexpr float top = OUT == kOutMx8 ? 448.f : 6.f;
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_fmed3f(v[i] * mul + 0.f, -top, top);
+  if constexpr (OUT == kOutMx8) {
+    int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w0, true);
+    int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
+    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], w1, true);
+    return make_uint2((uint32_t)w0, (uint32_t)w1);
+  } else {
+    uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, t[0], t[1], 1.f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[2], t[3], 1.f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[4], t[5], 1.f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[6], t[7], 1.f, 3);
+    return make_uint2(w, 0);
+  }
+}
+
+// E8M0 byte of a block from its largest magnitude's bits: the exponent field
+// less the element type's largest exponent (zero and fp32 subnormals: 0).
+template <int OUT>
+QMOE_D int mx_exponent(uint32_t max_bits) {
+  return max((int)(max_bits >> 23) - (OUT == kOutMx8 ? 8 : 2), 0);
+}
+// 2^-(e - 127), an fp32 normal for every byte in 0..252
+QMOE_D float mx_over(int e) { return __builtin_bit_cast(float, (uint32_t)(254 - e) << 23); }
+
+template <int OUT>
+QMOE_D void store_mx8(uint2 codes, int e, size_t at, void* out, void* scales) {
+  if constexpr (OUT == kOutMx8) *(uint2*)((uint8_t*)out + at) = codes;
+  else *(uint32_t*)((uint8_t*)out + (at >> 1)) = codes.x;
+  if ((threadIdx.x & 3) == 0) ((uint8_t*)scales)[at >> 5] = (uint8_t)e;
+}
+
 // Store one octet of row-major [R, K] values at flat index `at` (a multiple
 // of 8) in the output type.  Every lane of the block's four calls this.
-//  * MX: the shared exponent floor(log2 max) - emax is the exponent field of
-//    the largest magnitude less emax (zero and fp32 subnormals give byte 0);
-//    2^-E is an fp32 normal for every byte in 0..252, so scaling is exact, and
-//    the element conversions round to nearest even.  Clamping first makes
-//    them saturate; adding 0 turns a negative zero into a positive one.
+//  * MX: codes of v / 2^E, E from the block's largest magnitude; scaling by a
+//    power of two is exact.
 //  * int8: d = max * fp32(1 / 127), q = the quotient v / d (fp32) rounded half
 //    away from zero.
 template <int OUT>
@@ -96,27 +133,9 @@ QMOE_D void store_act8(const float (&v)[8], size_t at, void* out, void* scales) 
       *(uint2*)((int8_t*)out + at) = make_uint2(w[0], w[1]);
       if (first) ((float*)scales)[at >> 5] = bad ? __builtin_nanf("") : d;
     } else {
-      constexpr int emax = OUT == kOutMx8 ? 8 : 2;
-      const int e = max((int)(m >> 23) - emax, 0);
-      const float mul = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
-      constexpr float top = OUT == kOutMx8 ? 448.f : 6.f;
-      float t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_fmed3f(v[i] * mul + 0.f, -top, top);
-      if constexpr (OUT == kOutMx8) {
-        int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-        w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w0, true);
-        int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
-        w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], w1, true);
-        *(uint2*)((uint8_t*)out + at) = make_uint2(bad ? 0 : w0, bad ? 0 : w1);
-      } else {
-        uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, t[0], t[1], 1.f, 0);
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[2], t[3], 1.f, 1);
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[4], t[5], 1.f, 2);
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[6], t[7], 1.f, 3);
-        *(uint32_t*)((uint8_t*)out + (at >> 1)) = bad ? 0 : w;
-      }
-      if (first) ((uint8_t*)scales)[at >> 5] = (uint8_t)(bad ? 255 : e);
+      const int e = mx_exponent<OUT>(m);
+      const uint2 c = mx_codes8<OUT>(v, mx_over(e));
+      store_mx8<OUT>(bad ? make_uint2(0, 0) : c, bad ? 255 : e, at, out, scales);
     }
   }
 }

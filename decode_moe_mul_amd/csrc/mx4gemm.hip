@@ -33,8 +33,8 @@ QMOE_D v4f_t mma4(uint4 a, uint32_t sa, uint4 b, uint32_t sb, v4f_t c) {
 }
 
 // ------------------------------------------------------ few rows ------
-// A block computes 16 CT weight rows x 16 RT activation rows with 16x16x128
-// ops; its waves split K in turns of 512 values, and their sums meet in LDS in
+// A block computes 16 weight rows x 16 activation rows with 16x16x128 ops; its
+// waves split K in turns of 512 values, and their sums meet in LDS in
 // wave order.  Operands go from memory to registers, a whole turn's loads
 // together: with few rows the call is a read of the weights, and what counts is
 // how many of them are on their way.
@@ -70,93 +70,56 @@ QMOE_D void load_scales(const uint8_t* s, size_t row, int b0, int g, int nb, Fra
 
 constexpr int kRowsWaves = 8;
 
-template <int CT, int RT, bool YBF>
+template <bool YBF>
 __global__ __launch_bounds__(64 * kRowsWaves) void mxfp4_rows_kernel(Mx4Params P) {
-  extern __shared__ __align__(16) float red[];  // [wave][CT * RT][64 lanes][4]
+  __shared__ v4f_t sums[kRowsWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int nb = P.K >> 5, turns = (nb + 15) >> 4, full = nb >> 4;
-  const int n0 = blockIdx.x * 16 * CT, r0 = blockIdx.y * 16 * RT;
-  size_t wrow[CT], xrow[RT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) wrow[c] = (size_t)min(n0 + 16 * c + i, P.N - 1) * nb;
-#pragma unroll
-  for (int t = 0; t < RT; ++t) xrow[t] = (size_t)min(r0 + 16 * t + i, P.R - 1) * nb;
-  v4f_t acc[CT][RT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c)
-#pragma unroll
-    for (int t = 0; t < RT; ++t) acc[c][t] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  const int n0 = blockIdx.x * 16, r0 = blockIdx.y * 16;
+  const size_t wrow = (size_t)min(n0 + i, P.N - 1) * nb, xrow = (size_t)min(r0 + i, P.R - 1) * nb;
+  v4f_t acc = v4f_t{0.f, 0.f, 0.f, 0.f};
   const auto turn = [&](auto tail, int u) {
     constexpr bool TAIL = decltype(tail)::value;
-    Frag w[CT], x[RT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) load_scales<TAIL>(P.ws, wrow[c], 16 * u, g, nb, w[c]);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) load_scales<TAIL>(P.xs, xrow[t], 16 * u, g, nb, x[t]);
+    Frag w, x;
+    load_scales<TAIL>(P.ws, wrow, 16 * u, g, nb, w);
+    load_scales<TAIL>(P.xs, xrow, 16 * u, g, nb, x);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        load_codes<TAIL>(P.wq, wrow[c], 16 * u + 4 * j + g, nb, w[c].q[j]);
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-        load_codes<TAIL>(P.xq, xrow[t], 16 * u + 4 * j + g, nb, x[t].q[j]);
+      load_codes<TAIL>(P.wq, wrow, 16 * u + 4 * j + g, nb, w.q[j]);
+      load_codes<TAIL>(P.xq, xrow, 16 * u + 4 * j + g, nb, x.q[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          acc[c][t] = mma4(w[c].q[j], w[c].s[j], x[t].q[j], x[t].s[j], acc[c][t]);
+    for (int j = 0; j < 4; ++j) acc = mma4(w.q[j], w.s[j], x.q[j], x.s[j], acc);
   };
   int u = wave;
   for (; u < full; u += waves) turn(std::false_type{}, u);
   if (u < turns) turn(std::true_type{}, u);  // the last, partial turn
-  v4f_t* const sums = (v4f_t*)red;
-#pragma unroll
-  for (int c = 0; c < CT; ++c)
-#pragma unroll
-    for (int t = 0; t < RT; ++t) sums[(wave * CT * RT + c * RT + t) * 64 + lane] = acc[c][t];
+  sums[wave][lane] = acc;
   __syncthreads();
-  // lane 16 g + i of block (c, t) holds weight rows 16 c + 4 g .. + 3 of
-  // activation row 16 t + i
-  for (int o = threadIdx.x; o < CT * RT * 64; o += blockDim.x) {
-    v4f_t s = sums[o];
-    for (int w = 1; w < waves; ++w) {
-      const v4f_t v = sums[w * CT * RT * 64 + o];
+  if (wave > 0) return;
+  for (int w = 1; w < waves; ++w) {
+    const v4f_t v = sums[w][lane];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] += v[j];
-    }
-    const int l = o & 63, c = (o >> 6) / RT, t = (o >> 6) % RT;
-    const int r = r0 + 16 * t + (l & 15), n = n0 + 16 * c + 4 * (l >> 4);
-    if (r >= P.R) continue;
+    for (int j = 0; j < 4; ++j) acc[j] += v[j];
+  }
+  // lane 16 g + i: weight rows 4 g .. + 3 of activation row i
+  const int r = r0 + i, n = n0 + 4 * g;
+  if (r >= P.R) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + j >= P.N) break;
-      const size_t at = (size_t)r * P.N + n + j;
-      if constexpr (YBF) ((uint16_t*)P.y)[at] = (uint16_t)f32_to_bf16_bits(s[j]);
-      else ((float*)P.y)[at] = s[j];
-    }
+  for (int j = 0; j < 4; ++j) {
+    if (n + j >= P.N) break;
+    const size_t at = (size_t)r * P.N + n + j;
+    if constexpr (YBF) ((uint16_t*)P.y)[at] = (uint16_t)f32_to_bf16_bits(acc[j]);
+    else ((float*)P.y)[at] = acc[j];
   }
 }
 
-template <int CT, int RT>
 static int launch_rows(const Mx4Params& P, bool ybf, hipStream_t s) {
-  const dim3 grid((unsigned)((P.N + 16 * CT - 1) / (16 * CT)),
-                  (unsigned)((P.R + 16 * RT - 1) / (16 * RT)));
+  const dim3 grid((unsigned)((P.N + 15) / 16), (unsigned)((P.R + 15) / 16));
   const int waves = std::min(kRowsWaves, (P.K / 32 + 15) / 16);
-  const size_t lds = (size_t)waves * CT * RT * 64 * 16;
-  if (lds > (64u << 10))
-    (void)hipFuncSetAttribute(ybf ? (const void*)mxfp4_rows_kernel<CT, RT, true>
-                                  : (const void*)mxfp4_rows_kernel<CT, RT, false>,
-                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (ybf)
-    return QMOE_LAUNCH("mxfp4_rows", (mxfp4_rows_kernel<CT, RT, true>), grid, 64 * waves, lds, s,
-                       P);
-  return QMOE_LAUNCH("mxfp4_rows", (mxfp4_rows_kernel<CT, RT, false>), grid, 64 * waves, lds, s,
-                     P);
+  if (ybf) return QMOE_LAUNCH("mxfp4_rows", mxfp4_rows_kernel<true>, grid, 64 * waves, 0, s, P);
+  return QMOE_LAUNCH("mxfp4_rows", mxfp4_rows_kernel<false>, grid, 64 * waves, 0, s, P);
 }
 
 // ------------------------------------------------------ many rows ------
@@ -534,6 +497,45 @@ static int launch_tile(const Mx4Params& P, bool ybf, hipStream_t s) {
                      tm, tn);
 }
 
+// Which kernel.  A round of tiles takes about as long as one tile, so with K
+// given the choice goes by rounds times the time of one: as measured at K = 4096
+// (us), with `slots` tiles to a compute unit.
+//   rows   1 x 4096: 4.3, 16 x 4096: 5.1; 32 x 64: 6.6
+//   32 x 64, four teams  128 x 4096: 6.9;  64 x 64: 8.5;  64 x 128: 11
+//   64 x 64, four teams  64 x 14336: 10.7; 32 x 64: 15.0; 64 x 128: 14.8
+//   64 x 128, two teams  512 x 4096: 11.4; 64 x 64: 14.3; 128 x 128: 13.0
+//   128 x 128, two teams 256 x 14336: 15.2; 64 x 128: 20.9; 256 x 256: 28.6
+//   128 x 128, two to a unit  2048 x 4096: 25.4; two teams: 30.0; 256 x 256: 30.2
+//   256 x 256  2048 x 14336: 70; 128 x 128: 86
+static int launch_product(const Mx4Params& P, bool ybf, hipStream_t s) {
+  const int cus = std::max(1, cu_count());
+  if (P.R <= 16 && P.N <= 32 * cus) return launch_rows(P, ybf, s);
+  struct Choice {
+    int bm, bn, slots;
+    float us;
+    int (*launch)(const Mx4Params&, bool, hipStream_t);
+  };
+  static constexpr Choice choices[] = {
+      {32, 64, 1, 7.f, launch_tile<Tile<1, 2, 1, 1, 4>>},
+      {64, 64, 1, 9.5f, launch_tile<Tile<2, 2, 1, 1, 4>>},
+      {64, 128, 1, 11.f, launch_tile<Tile<2, 2, 1, 2, 2>>},
+      {128, 128, 1, 15.f, launch_tile<Tile<2, 2, 2, 2, 2>>},
+      {128, 128, 2, 25.f, launch_tile<Tile<2, 2, 2, 2, 1>>},
+      {256, 256, 1, 33.f, launch_tile<Tile<2, 2, 4, 4, 1>>}};
+  const Choice* best = nullptr;
+  float least = 0.f;
+  for (const Choice& c : choices) {
+    const long long tiles = (long long)((P.R + c.bm - 1) / c.bm) * ((P.N + c.bn - 1) / c.bn);
+    const long long at_once = (long long)c.slots * cus;
+    const float us = c.us * (float)((tiles + at_once - 1) / at_once);
+    if (!best || us < least) {
+      best = &c;
+      least = us;
+    }
+  }
+  return best->launch(P, ybf, s);
+}
+
 }  // namespace qmoe
 
 using namespace qmoe;
@@ -556,16 +558,5 @@ extern "C" int qgemm_mxfp4_mxfp4(const void* W, int N, int K, const uint8_t* cod
                     y, N, K, R};
   const bool ybf = y_dtype == QMOE_BF16;
   hipStream_t s = (hipStream_t)stream;
-  if ((R + 63) / 64 > 65535)
-    return fail(QMOE_ERR_UNSUPPORTED, "qgemm_mxfp4_mxfp4: R=%d too large", R);
-#ifdef ROWSV
-  return launch_rows<ROWSV>(P, ybf, s);
-#endif
-#ifdef VARIANT
-  return launch_tile<Tile<VARIANT>>(P, ybf, s);
-#endif
-  if (R > 256) return launch_tile<Tile<2, 2, 4, 4>>(P, ybf, s);
-  if (R <= 16) return launch_rows<1, 1>(P, ybf, s);
-  if (R <= 32) return launch_rows<2, 2>(P, ybf, s);
-  return launch_rows<4, 4>(P, ybf, s);
+  return launch_product(P, ybf, s);
 }

@@ -14,7 +14,10 @@ pytestmark = [pytest.mark.gpu, requires_gpu]
 # K that ends inside a step of 128 and inside a turn of 512
 SHAPES = [(1, 16, 32), (1, 1, 64), (1, 4096, 4096), (2, 49, 6752), (15, 130, 416), (16, 256, 512),
           (17, 33, 1056), (33, 640, 2048), (64, 2048, 640), (65, 100, 544), (130, 258, 1120),
-          (257, 384, 224), (300, 515, 7200), (513, 1030, 160)]
+          (257, 384, 224), (300, 515, 7200), (513, 1030, 160), (5, 9001, 288),
+          # one of each tile size, odd and even numbers of steps, one step
+          (300, 2001, 1312), (700, 2600, 352), (1000, 3900, 544), (2000, 4003, 800),
+          (2040, 8100, 256), (2047, 8101, 1056)]
 
 
 def _codes(rng, rows, K):
