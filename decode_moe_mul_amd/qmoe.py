@@ -471,73 +471,82 @@ def gemm_mxfp4_mxfp8(W, N, K, codes, scales, out=None):
 
 # ---------------------------------------------------- 4-bit activations --
 
-# These calls take a few microseconds on the GPU for a decode row, so their host
-# side is kept short: one test per tensor, pointers as plain ints, the raw
-# stream handle.
+# These calls take a few microseconds on the GPU for a decode row, and so do a
+# launch and each tensor that torch allocates.  Their own host side is kept
+# short: one condition over everything a call needs (what is wrong is worked out
+# only when something is), pointers as plain ints, the raw stream handle.
 
 ACT_FORMATS = ("q8", "mxfp8", "mxfp4")
-_ACT_TYPES = None   # format -> (values per code, code type, scale type)
+_th = None           # torch, once a call has needed it
+_FLOAT = {}          # output and activation types -> dtype codes
+_ACT_TYPES = {}      # format -> (values per code, code type, scale type)
 
 
-def _act_types():
-    global _ACT_TYPES
-    if _ACT_TYPES is None:
-        torch = _torch()
-        _ACT_TYPES = {"q8": (1, torch.int8, torch.float32), "mxfp8": (1, torch.uint8, torch.uint8),
-                      "mxfp4": (2, torch.uint8, torch.uint8)}
-    return _ACT_TYPES
+def _load_torch():
+    global _th
+    torch = _torch()
+    _FLOAT.update({torch.float32: F32, torch.bfloat16: BF16})
+    _ACT_TYPES.update({"q8": (1, torch.int8, torch.float32),
+                       "mxfp8": (1, torch.uint8, torch.uint8),
+                       "mxfp4": (2, torch.uint8, torch.uint8)})
+    _th = torch
+    return torch
 
 
 def _launch(name, index, *args):
     """Call entry point `name` with GPU `index` current, on that GPU's current
     stream."""
-    torch = _torch()
+    cuda = _th._C
     fn = getattr(_lib or lib(), name)
-    if index == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == cuda._cuda_getDevice():
+        st = fn(*args, cuda._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(index):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        with _th.cuda.device(index):
+            st = fn(*args, cuda._cuda_getCurrentRawStream(index))
     if st:
         _check(st, name)
 
 
-def _gpu(t, what):
-    """The GPU index of a contiguous tensor."""
-    _need(t.is_cuda and t.is_contiguous(), f"{what} must be a contiguous CUDA tensor")
-    return t.get_device()
+def _is(t, shape, dtype, index):
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous())
 
 
-def _require(t, shape, dtype, index, what):
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index
-            and t.is_contiguous()):
-        raise QmoeError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                        f"GPU {index}")
+def _refuse(what, t, shape, dtype, index):
+    """Raise for a tensor that _is not what it has to be."""
+    place = f"GPU {index}" if index >= 0 else "a GPU"
+    raise QmoeError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                    f"{place}, not {t.dtype} {tuple(t.shape)} on {t.device}"
+                    f"{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
-def _float_code(dtype, what):
-    torch = _torch()
-    if dtype is torch.float32:
-        return F32
-    if dtype is torch.bfloat16:
-        return BF16
-    raise QmoeError(f"{what} must be float32 or bfloat16, not {dtype}")
+def _rows(x, what):
+    """(R, K, GPU index, dtype code) of activations [R, K]."""
+    code, index = _FLOAT.get(x.dtype), x.get_device()
+    if code is None or index < 0 or x.dim() != 2 or not x.is_contiguous():
+        raise QmoeError(f"{what} must be a contiguous float32 or bfloat16 CUDA tensor [R, K], "
+                        f"not {x.dtype} {tuple(x.shape)} on {x.device}")
+    R, K = x.shape
+    return R, K, index, code
 
 
 def _float_out(out, dtype, like, shape, index):
     """(out, dtype code): a new tensor unless out is given."""
     if out is None:
-        dtype = _torch().float32 if dtype is None else dtype
-        code = _float_code(dtype, "outputs")
-        return like.new_empty(shape, dtype=dtype), code
-    code = _float_code(out.dtype, "outputs")
-    _require(out, shape, out.dtype if dtype is None else dtype, index, "out")
-    return out, code
+        dtype = _th.float32 if dtype is None else dtype
+    elif not _is(out, shape, out.dtype if dtype is None else dtype, index):
+        _refuse("out", out, shape, dtype or out.dtype, index)
+    else:
+        dtype = out.dtype
+    code = _FLOAT.get(dtype)
+    if code is None:
+        raise QmoeError(f"outputs are float32 or bfloat16, not {dtype}")
+    return (like.new_empty(shape, dtype=dtype) if out is None else out), code
 
 
 def _act_out(fmt, like, R, K, index, out):
     """(codes, scales) of activation format `fmt` for [R, K]."""
-    kinds = _act_types().get(fmt)
+    kinds = _ACT_TYPES.get(fmt)
     if kinds is None:
         raise QmoeError(f"activation format {fmt!r} is not one of {ACT_FORMATS}")
     if K <= 0 or K % 32:
@@ -545,30 +554,30 @@ def _act_out(fmt, like, R, K, index, out):
     per, ct, st = kinds
     if out is None:
         return like.new_empty((R, K // per), dtype=ct), like.new_empty((R, K // 32), dtype=st)
-    _require(out[0], (R, K // per), ct, index, "codes")
-    _require(out[1], (R, K // 32), st, index, "scales")
-    return out
+    codes, scales = out
+    if not _is(codes, (R, K // per), ct, index):
+        _refuse("codes", codes, (R, K // per), ct, index)
+    if not _is(scales, (R, K // 32), st, index):
+        _refuse("scales", scales, (R, K // 32), st, index)
+    return codes, scales
 
 
-def _act_in(codes, scales):
-    """(R, K, GPU index) of MXFP4 activations."""
-    torch = _torch()
-    _need(codes.dim() == 2, "codes must be [R, K/2]")
-    R, K = codes.shape
-    K *= 2
-    index = _gpu(codes, "codes")
-    _require(codes, (R, K // 2), torch.uint8, index, "codes")
-    _require(scales, (R, K // 32), torch.uint8, index, "scales")
-    return R, K, index
+def _act_in(codes, scales, K):
+    """(R, GPU index) of MXFP4 activations [R, K]."""
+    u8, index, R = _th.uint8, codes.get_device(), codes.shape[0] if codes.dim() else 0
+    if index < 0 or not _is(codes, (R, K // 2), u8, index):
+        _refuse("codes", codes, (R, K // 2), u8, index)
+    if not _is(scales, (R, K // 32), u8, index):
+        _refuse("scales", scales, (R, K // 32), u8, index)
+    return R, index
 
 
 def quantize_act_mxfp4(x, out=None):
     """Activations [R, K] (float32 or bfloat16) -> MXFP4 codes [R, K/2] uint8
     (two E2M1 codes per byte, low nibble first) and scales [R, K/32] uint8
     (E8M0)."""
-    _need(x.dim() == 2, "x must be [R, K]")
-    R, K = x.shape
-    index, xd = _gpu(x, "x"), _float_code(x.dtype, "activations")
+    _th or _load_torch()
+    R, K, index, xd = _rows(x, "x")
     codes, scales = _act_out("mxfp4", x, R, K, index, out)
     _launch("qquantize_act_mxfp4", index, x.data_ptr(), xd, R, K, codes.data_ptr(),
             scales.data_ptr())
@@ -578,7 +587,9 @@ def quantize_act_mxfp4(x, out=None):
 def dequantize_act_mxfp4(codes, scales, dtype=None, out=None):
     """The values [R, K] of MXFP4 activations (float32 unless dtype says
     bfloat16)."""
-    R, K, index = _act_in(codes, scales)
+    _th or _load_torch()
+    K = 2 * codes.shape[-1] if codes.dim() else 0
+    R, index = _act_in(codes, scales, K)
     out, yd = _float_out(out, dtype, codes, (R, K), index)
     _launch("qdequant_act_mxfp4", index, codes.data_ptr(), scales.data_ptr(), R, K,
             out.data_ptr(), yd)
@@ -586,21 +597,24 @@ def dequantize_act_mxfp4(codes, scales, dtype=None, out=None):
 
 
 def _norm_args(x, w, eps, res, res_out):
-    _need(x.dim() == 2, "x must be [R, K]")
-    R, K = x.shape
-    index, xd = _gpu(x, "x"), _float_code(x.dtype, "activations")
-    _require(w, (K,), _torch().float32, index, "w")
+    R, K, index, xd = _rows(x, "x")
+    f32 = _th.float32
+    if not _is(w, (K,), f32, index):
+        _refuse("w", w, (K,), f32, index)
     if res is None:
-        _need(res_out is None, "res_out without res")
+        if res_out is not None:
+            raise QmoeError("res_out without res")
         return index, R, K, None, (x.data_ptr(), xd, None, None, 0, w.data_ptr(), eps, R, K)
-    rd = _float_code(res.dtype, "res")
-    _require(res, (R, K), res.dtype, index, "res")
+    rd, shape = _FLOAT.get(res.dtype), x.shape
+    if rd is None or not _is(res, shape, res.dtype, index):
+        _refuse("res", res, shape, "float32 or bfloat16", index)
+    at = res.data_ptr()
     if res_out is None:
-        res_out = _torch().empty_like(res)
-    elif res_out is not res:
-        _require(res_out, (R, K), res.dtype, index, "res_out")
-    return index, R, K, res_out, (x.data_ptr(), xd, res.data_ptr(), res_out.data_ptr(), rd,
-                                  w.data_ptr(), eps, R, K)
+        res_out = _th.empty_like(res)
+    elif res_out is not res and not _is(res_out, shape, res.dtype, index):
+        _refuse("res_out", res_out, shape, res.dtype, index)
+    return index, R, K, res_out, (x.data_ptr(), xd, at, res_out.data_ptr(), rd, w.data_ptr(),
+                                  eps, R, K)
 
 
 def norm(x, w, eps, res=None, res_out=None, dtype=None, out=None):
@@ -608,6 +622,7 @@ def norm(x, w, eps, res=None, res_out=None, dtype=None, out=None):
     sqrt(mean(h^2) + eps) in float32, or dtype.  Returns y, with res (y, h);
     h has res' type and goes to res_out (a new tensor unless given; res itself
     for an update in place)."""
+    _th or _load_torch()
     index, R, K, h, args = _norm_args(x, w, eps, res, res_out)
     out, yd = _float_out(out, dtype, x, (R, K), index)
     _launch("qnorm", index, *args, out.data_ptr(), yd)
@@ -617,6 +632,7 @@ def norm(x, w, eps, res=None, res_out=None, dtype=None, out=None):
 def norm_act(fmt, x, w, eps, res=None, res_out=None, out=None):
     """norm's float32 rows in activation format fmt ("q8", "mxfp8", "mxfp4"):
     (codes, scales), with res (codes, scales, h)."""
+    _th or _load_torch()
     index, R, K, h, args = _norm_args(x, w, eps, res, res_out)
     codes, scales = _act_out(fmt, x, R, K, index, out)
     _launch("qnorm_act_" + fmt, index, *args, codes.data_ptr(), scales.data_ptr())
@@ -627,18 +643,20 @@ def swiglu_act(fmt, gate, up, out=None):
     """gate / (1 + exp(-gate)) * up [R, K] in activation format fmt: (codes,
     scales).  gate and up are float32 or bfloat16, with contiguous rows; the
     rows may lie further apart (the two halves of one [R, 2K] tensor)."""
-    _need(gate.dim() == 2 and gate.is_cuda and gate.shape == up.shape and gate.dtype is up.dtype
-          and gate.get_device() == up.get_device(),
-          "gate and up must be CUDA tensors [R, K] of one type on one GPU")
-    R, K = gate.shape
-    index, xd = gate.get_device(), _float_code(gate.dtype, "gate and up")
+    _th or _load_torch()
+    xd, index, shape = _FLOAT.get(gate.dtype), gate.get_device(), gate.shape
+    if (xd is None or index < 0 or len(shape) != 2 or up.shape != shape
+            or up.dtype is not gate.dtype or up.get_device() != index):
+        raise QmoeError("gate and up must be float32 or bfloat16 CUDA tensors [R, K] of one "
+                        "type on one GPU")
+    R, K = shape
     ld = K
     if R > 0:
         (ld, one), (ld_up, one_up) = gate.stride(), up.stride()
         if R == 1:
             ld = ld_up = K   # the distance of a single row says nothing
-        _need(one == one_up == 1 and ld == ld_up,
-              "gate and up must have contiguous rows, equally far apart")
+        if one != 1 or one_up != 1 or ld != ld_up:
+            raise QmoeError("gate and up must have contiguous rows, equally far apart")
     codes, scales = _act_out(fmt, gate, R, K, index, out)
     _launch("qswiglu_act_" + fmt, index, gate.data_ptr(), up.data_ptr(), xd, ld, R, K,
             codes.data_ptr(), scales.data_ptr())
@@ -648,11 +666,11 @@ def swiglu_act(fmt, gate, up, out=None):
 def gemm_mxfp4_mxfp4(W, N, K, codes, scales, dtype=None, out=None):
     """y [R, N] (float32 unless dtype says bfloat16) = W (MXFP4 [N, K]) times
     the MXFP4 activations; R from one decode row to a prefill chunk."""
-    R, K2, index = _act_in(codes, scales)
-    _need(K2 == K, f"the activations have {K2} values a row, the weights {K}")
-    _need(N >= 0 and W.dtype is codes.dtype and W.get_device() == index and W.is_contiguous()
-          and W.numel() >= -(-N * K // 512) * 256 + -(-N * K // 8192) * 256,
-          "W must be a packed MXFP4 [N, K] tensor on the activations' GPU")
+    _th or _load_torch()
+    R, index = _act_in(codes, scales, K)
+    if (N < 0 or W.dtype is not codes.dtype or W.get_device() != index or not W.is_contiguous()
+            or W.numel() < -(-N * K // 512) * 256 + -(-N * K // 8192) * 256):
+        raise QmoeError("W must be a packed MXFP4 [N, K] tensor on the activations' GPU")
     out, yd = _float_out(out, dtype, codes, (R, N), index)
     _launch("qgemm_mxfp4_mxfp4", index, W.data_ptr(), N, K, codes.data_ptr(), scales.data_ptr(),
             R, out.data_ptr(), yd)

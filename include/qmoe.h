@@ -413,7 +413,7 @@ int qgemm_q8_0_i8(const void *W, int N, int K, const int8_t *q, const float *d,
  *   correctly rounded one (but for values within 2^-50 of a rounding border).
  *   x [R, K] (x_dtype), res and res_out [R, K] (res_dtype, ignored without
  *   res), w [K] fp32, y [R, K].  res_out may be NULL, or res itself (in
- *   place); no other output may overlap an input.
+ *   place).
  * qnorm_act_<fmt>: the activation quantizer of <fmt> applied to the fp32 y.
  *   All pointers 16-byte aligned (mxfp scales: any; d: 4-byte).
  *   Limits: K <= 32768, K % 32 == 0 (qnorm: K % 8 == 0), eps >= 0.
@@ -427,8 +427,10 @@ int qgemm_q8_0_i8(const void *W, int N, int K, const int8_t *q, const float *d,
  * qgemm_mxfp4_mxfp4: y [R, N] (y_dtype) = sum_k w[n, k] * x[r, k] for MXFP4
  *   weights W [N, K] (qmoe layout, 256-byte aligned) and MXFP4 activations;
  *   products are exact, sums are fp32 in the matrix cores, rounded once to
- *   y_dtype.  Any R and N; K % 32 == 0, K <= 65536.  codes and y 16-byte
- *   aligned, scales any.
+ *   y_dtype.  R, N <= 2^30; K % 32 == 0, K <= 65536.  codes and y 16-byte
+ *   aligned, scales any.  The tile that R and N call for may sum in another
+ *   order, so a row's last bits can depend on R.
+ * No output may overlap an input or another output, but for res_out == res.
  * Errors: INVALID_ARG for sizes, null pointers and misalignment; UNSUPPORTED
  *   for unknown dtypes and sizes beyond a limit.                             */
 #define QMOE_NORM_ARGS                                                          \

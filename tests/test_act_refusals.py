@@ -73,6 +73,7 @@ def test_product(L):
                 dict(y=A + 4)):
         assert g(**bad) == BAD, bad
     assert g(yd=2) == UNSUP
+    assert g(N=(1 << 30) + 1) == UNSUP and g(R=(1 << 30) + 1) == UNSUP
 
 
 def test_the_binding_refuses_what_the_kernels_cannot_take():
@@ -84,6 +85,8 @@ def test_the_binding_refuses_what_the_kernels_cannot_take():
                  lambda: qmoe.swiglu_act("q8", x, x[:, :32]),              # shapes differ
                  lambda: qmoe.swiglu_act("q8", x, x.bfloat16()),           # types differ
                  lambda: qmoe.dequantize_act_mxfp4(x, x),                  # not codes
+                 lambda: qmoe.dequantize_act_mxfp4(torch.tensor(1), x),
+                 lambda: qmoe.norm_act("q8", x, torch.ones(64), 1e-5, res_out=x),
                  lambda: qmoe.gemm_mxfp4_mxfp4(torch.zeros(8, dtype=torch.uint8), 16, 64,
                                                torch.zeros(4, 32, dtype=torch.uint8),
                                                torch.zeros(4, 2, dtype=torch.uint8))):

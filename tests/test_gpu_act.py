@@ -132,6 +132,19 @@ def test_norm_types(xbf, res, fmt):
             assert_bitexact(to_np(gr.float()), h)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_norm_of_x_added_to_itself_in_place(fmt):
+    """x, res and res_out are one tensor: h = 2 x."""
+    x = _x((40, 2080), 22)
+    w = np.ones(2080, np.float32)
+    g = to_gpu(x)
+    q, s, h = qmoe.norm_act(fmt, g, to_gpu(w), 1e-5, res=g, res_out=g)
+    y, rh = act.rms_norm(x, w, 1e-5, x)
+    _same_act((q, s), act.quantize(fmt, y))
+    assert h is g
+    assert_bitexact(to_np(g), rh)
+
+
 def test_plain_norm_of_a_width_that_is_no_multiple_of_32():
     x, w = _x((5, 1000), 10), 1 + _x((1, 1000), 11, 0.1)[0]
     assert_bitexact(to_np(qmoe.norm(to_gpu(x), to_gpu(w), 1e-5)), act.rms_norm(x, w, 1e-5)[0])

@@ -98,7 +98,42 @@ def test_nothing_is_written_behind_the_last_row(R, N, bf):
     assert torch.equal(big[:R], qmoe.gemm_mxfp4_mxfp4(W, N, K, c, s, dtype=dt))
 
 
-def test_rows_do_not_depend_on_their_neighbours():
+@pytest.mark.parametrize("R,N,K", [(3, 70, 1056), (100, 130, 1056), (2040, 8100, 288)])
+def test_scales_at_any_address(R, N, K):
+    """Scale rows have K / 32 bytes and start anywhere: here at an odd address."""
+    rng = np.random.default_rng(8)
+    q, wq = _codes(rng, R, K), _codes(rng, N, K)
+    e, we = (rng.integers(126, 129, (n, K // 32)).astype(np.uint8) for n in (R, N))
+    W, codes = to_gpu(_w(wq, we, N, K)), to_gpu(act.pack_codes(q))
+    want = qmoe.gemm_mxfp4_mxfp4(W, N, K, codes, to_gpu(e))
+    odd = torch.zeros(e.size + 1, dtype=torch.uint8, device="cuda")
+    odd[1:] = to_gpu(e).view(-1)
+    scales = odd[1:].view(e.shape)
+    assert scales.data_ptr() % 2 == 1
+    assert torch.equal(want, qmoe.gemm_mxfp4_mxfp4(W, N, K, codes, scales))
+
+
+def test_calls_on_two_streams_at_once():
+    """No state is shared between calls: two streams at work together give what
+    each gives alone."""
+    N, K = 1030, 2080
+    W = qmoe.quantize("mxfp4", to_gpu(synth.normal((N, K), 0.02, 5, synth.GATE, 0)))
+    acts = [qmoe.quantize_act_mxfp4(to_gpu(synth.normal((R, K), 1.0, R, synth.ACT, R)))
+            for R in (9, 700)]
+    want = [qmoe.gemm_mxfp4_mxfp4(W, N, K, *a) for a in acts]
+    streams = [torch.cuda.Stream() for _ in acts]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (st, a) in enumerate(zip(streams, acts)):
+            with torch.cuda.stream(st):
+                got[i].append(qmoe.gemm_mxfp4_mxfp4(W, N, K, *a))
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
+
+
+def test_the_same_call_twice_gives_the_same_bits():
     """Two calls in turn give the same bits, and an empty one writes nothing."""
     N, K, R = 258, 1056, 270
     W = qmoe.quantize("mxfp4", to_gpu(synth.normal((N, K), 0.02, 5, synth.GATE, 0)))
