@@ -144,7 +144,7 @@ static int launch_rows(const Mx4Params& P, bool ybf, hipStream_t s) {
 //  * scales pass through registers (their rows have any alignment): 16 bytes a
 //    row serve two steps, in one of two LDS buffers; a byte permute gives each
 //    lane its four blocks of a step in one word, whose bytes the ops select.
-// The 16-byte chunk c of tile row q lies at chunk c ^ (q & 7), chosen by
+// The 16-byte chunk c of tile row q lies at chunk c ^ ((q >> 1) & 7), chosen by
 // which chunk of memory a lane fetches, so that the rows one operand read
 // touches spread over the banks.  Rows past the ends repeat the last one and
 // are never stored; blocks past K's end repeat the row's last one with scale
@@ -163,7 +163,7 @@ struct Tile {
   static constexpr int JA = BM / 8 / NW, J = ROWS / 8 / NW;     // copies per wave and step
   static constexpr int J1 = J / 2;                              // of them in the first part
   static constexpr int SR = (ROWS + TEAM - 1) / TEAM;           // scale rows per thread
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "");
+  static_assert(NW % 2 == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "");
   // leaving: 32 rows of a wave's columns, then the other teams' sums
   static constexpr int COLS = 32 * TN, PITCH = COLS + 8, OUT = NW * 32 * PITCH * 4;
   static constexpr int SUMS = TM * TN * 16 * TEAM * 4;
@@ -228,10 +228,10 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
   const uint8_t* const bbase = P.wq + (size_t)n0 * rowb;
   const int arows = P.R - r0 - 1, brows = P.N - n0 - 1;  // last valid row of the tile
 
-  // Copy j of the wave fills tile rows 8 (wave + NW j) .. + 7, so the lane's
-  // chunk is the same for every j.
+  // Copy j of the wave fills tile rows 8 (wave + NW j) .. + 7, and NW is even,
+  // so the lane's chunk is the same for every j.
   const int rem = nb - 8 * (all - 1);  // blocks of K's last step, 1..8
-  const int chunk = (lane & 7) ^ (lane >> 3);
+  const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
   const uint32_t over = 16u * (uint32_t)max(chunk - (rem - 1), 0);
   uint32_t off[T::J];
 #pragma unroll
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
   const auto row_of = [&](int r) { return r < TM ? qa + 32 * r : qb + 32 * (r - TM); };
   const auto read_op = [&](int st, int s, int r, Ops& o) {
     o.v[r] = *(const uint4*)(mem + (st & 1) * T::CODES + row_of(r) * 128 +
-                             16 * ((2 * s + h) ^ (i & 7)));
+                             16 * ((2 * s + h) ^ ((i >> 1) & 7)));
   };
   uint2 raw[NR];  // a row's scales of the next step
   const auto read_raw = [&](int st, int r) {
