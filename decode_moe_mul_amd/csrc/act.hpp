@@ -104,6 +104,24 @@ QMOE_D void store_mx8(uint2 codes, int e, size_t at, void* out, void* scales) {
   if ((threadIdx.x & 3) == 0) ((uint8_t*)scales)[at >> 5] = (uint8_t)e;
 }
 
+// Eight int8 codes: the fp32 quotients v / d rounded half away from zero.  With
+// the reciprocal of d rounded to nearest (one division), a quotient is the
+// product, corrected once by its exact remainder: rounded to nearest by
+// Markstein's theorem, and a third of eight divisions' work (norm 8192 x 7168 to
+// int8 106 us with those).  Small d are scaled up first, exactly, to keep the
+// remainder above the subnormals.
+QMOE_D void q8_codes8(const float (&v)[8], float d, uint32_t (&w)[2]) {
+  const float up = d < 0x1p-60f ? 0x1p90f : 1.f, ds = d * up, rd = 1.f / ds;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = v[i] * up, q1 = a * rd, q = fmaf(fmaf(-q1, ds, a), rd, q1);
+    const float t = truncf(q);
+    const float c = t + (fabsf(q - t) >= 0.5f ? copysignf(1.f, q) : 0.f);
+    w[i >> 2] |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(c, -127.f, 127.f) & 0xFFu)
+                 << (8 * (i & 3));
+  }
+}
+
 // Store one octet of row-major [R, K] values at flat index `at` (a multiple
 // of 8) in the output type.  Every lane of the block's four calls this.
 //  * MX: codes of v / 2^E, E from the block's largest magnitude; scaling by a
@@ -121,15 +139,8 @@ QMOE_D void store_act8(const float (&v)[8], size_t at, void* out, void* scales) 
     if constexpr (OUT == kOutQ8) {
       const float d = __builtin_bit_cast(float, m) * (1.f / 127.f);
       uint32_t w[2] = {0, 0};
-      if (d > 0.f && !bad) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float r = v[i] / d, t = truncf(r);
-          int c = (int)t + (fabsf(r - t) >= 0.5f ? (r < 0.f ? -1 : 1) : 0);
-          c = min(max(c, -127), 127);
-          w[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
-        }
-      }
+      q8_codes8(v, d, w);
+      if (!(d > 0.f) || bad) w[0] = w[1] = 0;
       *(uint2*)((int8_t*)out + at) = make_uint2(w[0], w[1]);
       if (first) ((float*)scales)[at >> 5] = bad ? __builtin_nanf("") : d;
     } else {

@@ -10,7 +10,8 @@
 // by several units.  The sum of squares (a square of fp32 is exact in fp64),
 // the root and the product are therefore fp64, rounded once to fp32; fp64
 // multiply-adds run at the rate of fp32 ones on this part, and the kernel
-// stays bound by memory.
+// stays bound by memory: 8192 x 7168 bf16 to MXFP8, 413 MB, in 89-92 us (4.5 TB/s; a
+// 1 GiB copy moves 5.1).
 #include <algorithm>
 
 #include "act.hpp"
@@ -30,13 +31,19 @@ struct NormParams {
   int R, K;
 };
 
-QMOE_D double wave_sum(double v) {
+// Sum over aligned groups of `lanes` lanes (a power of two; a wave or more: the
+// wave's).
+QMOE_D double lanes_sum(double v, int lanes) {
+  if (lanes >= 64) {
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  } else {
+    for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  }
   return v;
 }
 
-// tpr threads share a row (a power of two, at least a wave), NPT octets each:
+// tpr threads share a row (a power of two, a block's four at least), NPT octets each:
 // octet o of the row belongs to thread o mod tpr.  A block takes
 // blockDim.x / tpr rows at a time and goes on to later ones.  w is requested
 // with the row where a thread has one or two octets (one wait for memory, few
@@ -48,7 +55,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams P, int tpr) {
   const int K8 = P.K >> 3;
   const int t = threadIdx.x & (tpr - 1), lrow = threadIdx.x / tpr;
   const int rows = blockDim.x / tpr;
-  const int waves = tpr >> 6, wave0 = (threadIdx.x >> 6) & ~(waves - 1);
+  const int waves = tpr >> 6, wave0 = (threadIdx.x >> 6) & ~(waves - 1);  // used with two or more
   constexpr bool early = NPT <= 2;
   // uniform over the block: every thread meets the barriers the same number of times
   for (long long r0 = (long long)blockIdx.x * rows; r0 < P.R; r0 += (long long)gridDim.x * rows) {
@@ -82,7 +89,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams P, int tpr) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fma((double)h[j][i], (double)h[j][i], sum);
     }
-    sum = wave_sum(sum);
+    sum = lanes_sum(sum, tpr);
     if (waves > 1) {
       __syncthreads();  // the last row's sums have been read
       if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
@@ -141,9 +148,13 @@ static int run_norm(const char* who, const void* x, int x_dtype, const void* res
       (OUT == kOutQ8 && !QMOE_ALIGNED(scales, 4)))
     return fail(QMOE_ERR_INVALID_ARG, "%s: misaligned pointer", who);
   const int K8 = K >> 3, cus = std::max(1, cu_count());
-  // One octet per thread while the rows leave the part idle (latency), up to
-  // four once they fill it (fewer barriers and sums per byte).
-  int npt = R > 4 * cus ? 4 : 1, tpr = 64;
+  // Octets per thread.  Rows up to 4096 take one: 2048 x 2048 fp32 to MXFP8 12.3
+  // us, with four 13.7; 1 x 4096 3.3 and 4.1.  Longer rows take two while there
+  // are few of them (16 x 7168 bf16 4.2; one 4.5, four 5.3) and four once they
+  // fill the part (8192 x 7168 92, two 95, one 97; 1024 x 7168 13.8, 14.9, 14.9):
+  // fewer barriers and sums per byte.  Rows below 512 share a wave: 8192 x 256 5.5
+  // us, with a wave to each 7.2.
+  int npt = K8 <= 512 ? 1 : R <= 2 * cus ? 2 : 4, tpr = 4;
   while (tpr < 1024 && tpr * npt < K8) tpr *= 2;
   while (tpr * npt < K8) npt *= 2;  // longer rows than 1024 threads hold: more per thread
   const int block = std::max(tpr, 256), rows = block / tpr;

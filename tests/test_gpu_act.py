@@ -87,7 +87,8 @@ def test_read_back_of_every_code_and_scale():
 # one octet per thread, several waves a row, rows not a multiple of a block's,
 # two and four octets per thread, several rows to a block in turn
 SIZES = [(1, 32), (1, 4096), (3, 96), (5, 2080), (300, 2048), (2, 7168), (3, 8224), (2, 16416),
-         (1, 32768), (1100, 160), (2100, 2080), (1031, 8224), (4500, 32)]
+         (1, 32768), (1100, 160), (2100, 2080), (1031, 8224), (4500, 32),
+         (70, 64), (1000, 224), (9, 480), (600, 7168)]
 
 
 @pytest.mark.parametrize("R,K", SIZES)
@@ -130,6 +131,21 @@ def test_norm_types(xbf, res, fmt):
         if gr is not None:
             assert got[-1] is gr
             assert_bitexact(to_np(gr.float()), h)
+
+
+def test_int8_codes_at_halves_and_with_tiny_scales():
+    """Quotients on and next to k + 1/2, and scales down to the smallest
+    subnormal: the block's largest value pins d."""
+    k = np.arange(127, dtype=np.float32)
+    v = np.concatenate([k + 0.5, np.nextafter(k + 0.5, 0), np.nextafter(k + 0.5, 200)])
+    v = np.concatenate([v, -v]).astype(np.float32)
+    v = np.concatenate([v, np.zeros(-len(v) % 31, np.float32)]).reshape(-1, 31)
+    x = np.concatenate([np.full((len(v), 1), 127, np.float32), v], axis=1).reshape(1, -1)
+    x = np.concatenate([x * np.float32(2.0) ** e for e in (0, 17, -60, -101, -126, -140)])
+    x = np.pad(x, ((0, 0), (0, -x.shape[1] % 32)))
+    # SwiGLU with a gate of 64 is 64 up, to fp32's last bit
+    g, u = np.full_like(x, 64.0), x / np.float32(64.0)
+    _same_act(qmoe.swiglu_act("q8", to_gpu(g), to_gpu(u)), act.quantize("q8", act.swiglu(g, u)))
 
 
 @pytest.mark.parametrize("fmt", FMTS)
