@@ -53,17 +53,26 @@ __global__ __launch_bounds__(256) void dequantize_act_mxfp4_kernel(const uint8_t
 // for every finite gate and up.
 QMOE_D float swiglu1(float g, float u) {
   const double z = fmin(fmax(-(double)g, -60.0), 700.0);
-  const double n = rint(z * 1.4426950408889634);
-  double r = fma(n, -6.93147180369123816490e-01, z);  // ln 2's upper bits: n times it is exact
-  r = fma(n, -1.90821492927058770002e-10, r);
+  // adding 1.5 * 2^52 rounds to an integer, which the sum's low word holds
+  const double sum = fma(z, 1.4426950408889634, 6755399441055744.0);
+  const int32_t ni = (int32_t)(uint32_t)__builtin_bit_cast(uint64_t, sum);
+  const double n = sum - 6755399441055744.0;
+  double r = fma(n, -0x1.62e42fefa4000p-1, z);  // ln 2 to 40 bits: n times it is exact
+  r = fma(n, 0x1.8432a1b0e2634p-43, r);               // and the rest (Cody and Waite's reduction)
   constexpr double c[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720,
                             1.0 / 5040, 1.0 / 40320, 1.0 / 362880, 1.0 / 3628800,
                             1.0 / 39916800, 1.0 / 479001600, 1.0 / 6227020800};
   double p = c[13];
 #pragma unroll
   for (int i = 12; i >= 0; --i) p = fma(p, r, c[i]);
-  const double den = 1.0 + ldexp(p, (int)n);
-  return (float)((double)g * (double)u / den);
+  const uint64_t bits = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(uint32_t)ni << 52);
+  const double den = 1.0 + __builtin_bit_cast(double, bits);
+  // the hardware's reciprocal, within 2^-20, and two Newton steps: 2^-80 but
+  // for their own rounding
+  double y = __builtin_amdgcn_rcp(den);
+  y = fma(fma(-den, y, 1.0), y, y);
+  y = fma(fma(-den, y, 1.0), y, y);
+  return (float)((double)g * (double)u * y);
 }
 
 // The same in fp32, within kGluErr of it (relative) for finite results of
