@@ -477,14 +477,16 @@ def gemm_mxfp4_mxfp8(W, N, K, codes, scales, out=None):
 # only when something is), pointers as plain ints, the raw stream handle.
 
 ACT_FORMATS = ("q8", "mxfp8", "mxfp4")
-_th = None           # torch, once a call has needed it
+_th = None           # torch, once a call has needed it, and two of its functions
+_device = _stream_of = None
 _FLOAT = {}          # output and activation types -> dtype codes
 _ACT_TYPES = {}      # format -> (values per code, code type, scale type)
 
 
 def _load_torch():
-    global _th
+    global _th, _device, _stream_of
     torch = _torch()
+    _device, _stream_of = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _FLOAT.update({torch.float32: F32, torch.bfloat16: BF16})
     _ACT_TYPES.update({"q8": (1, torch.int8, torch.float32),
                        "mxfp8": (1, torch.uint8, torch.uint8),
@@ -496,13 +498,12 @@ def _load_torch():
 def _launch(name, index, *args):
     """Call entry point `name` with GPU `index` current, on that GPU's current
     stream."""
-    cuda = _th._C
     fn = getattr(_lib or lib(), name)
-    if index == cuda._cuda_getDevice():
-        st = fn(*args, cuda._cuda_getCurrentRawStream(index))
+    if index == _device():
+        st = fn(*args, _stream_of(index))
     else:
         with _th.cuda.device(index):
-            st = fn(*args, cuda._cuda_getCurrentRawStream(index))
+            st = fn(*args, _stream_of(index))
     if st:
         _check(st, name)
 
