@@ -488,8 +488,6 @@ __global__ __launch_bounds__(T::THREADS) void mxfp4_tile_kernel(Mx4Params P, int
 template <class T>
 static int launch_tile(const Mx4Params& P, bool ybf, hipStream_t s) {
   const int tm = (P.R + T::BM - 1) / T::BM, tn = (P.N + T::BN - 1) / T::BN;
-  if ((long long)tm * tn > 1 << 30)
-    return fail(QMOE_ERR_UNSUPPORTED, "qgemm_mxfp4_mxfp4: too many tiles");
   const dim3 grid((unsigned)(tm * tn));
   // a kernel that takes more than 64 KB of LDS declares it, once per device
   static std::atomic<uint64_t> declared[2];
@@ -509,6 +507,16 @@ static int launch_tile(const Mx4Params& P, bool ybf, hipStream_t s) {
                      tm, tn);
 }
 
+struct Choice {
+  int bm, bn, threads, slots;
+  float us;
+  int (*launch)(const Mx4Params&, bool, hipStream_t);
+};
+template <class T>
+static constexpr Choice choice(int slots, float us) {
+  return {T::BM, T::BN, T::THREADS, slots, us, launch_tile<T>};
+}
+
 // Which kernel.  A round of tiles takes about as long as one tile, so with K
 // given the choice goes by rounds times the time of one: as measured at K = 4096
 // (us), with `slots` tiles to a compute unit.
@@ -519,25 +527,19 @@ static int launch_tile(const Mx4Params& P, bool ybf, hipStream_t s) {
 //   128 x 128, two teams 256 x 14336: 15.2; 64 x 128: 20.9; 256 x 256: 28.6
 //   128 x 128, two to a unit  2048 x 4096: 25.4; two teams: 30.0; 256 x 256: 30.2
 //   256 x 256  2048 x 14336: 70; 128 x 128: 86
+// A launch has fewer than 2^32 threads: a tile that would need more is passed over.
 static int launch_product(const Mx4Params& P, bool ybf, hipStream_t s) {
   const int cus = std::max(1, cu_count());
   if (P.R <= 16 && P.N <= 32 * cus) return launch_rows(P, ybf, s);
-  struct Choice {
-    int bm, bn, slots;
-    float us;
-    int (*launch)(const Mx4Params&, bool, hipStream_t);
-  };
   static constexpr Choice choices[] = {
-      {32, 64, 1, 7.f, launch_tile<Tile<1, 2, 1, 1, 4>>},
-      {64, 64, 1, 9.5f, launch_tile<Tile<2, 2, 1, 1, 4>>},
-      {64, 128, 1, 11.f, launch_tile<Tile<2, 2, 1, 2, 2>>},
-      {128, 128, 1, 15.f, launch_tile<Tile<2, 2, 2, 2, 2>>},
-      {128, 128, 2, 25.f, launch_tile<Tile<2, 2, 2, 2, 1>>},
-      {256, 256, 1, 33.f, launch_tile<Tile<2, 2, 4, 4, 1>>}};
+      choice<Tile<1, 2, 1, 1, 4>>(1, 7.f),  choice<Tile<2, 2, 1, 1, 4>>(1, 9.5f),
+      choice<Tile<2, 2, 1, 2, 2>>(1, 11.f), choice<Tile<2, 2, 2, 2, 2>>(1, 15.f),
+      choice<Tile<2, 2, 2, 2, 1>>(2, 25.f), choice<Tile<2, 2, 4, 4, 1>>(1, 33.f)};
   const Choice* best = nullptr;
   float least = 0.f;
   for (const Choice& c : choices) {
     const long long tiles = (long long)((P.R + c.bm - 1) / c.bm) * ((P.N + c.bn - 1) / c.bn);
+    if (tiles > 0xFFFFFFFFLL / c.threads) continue;
     const long long at_once = (long long)c.slots * cus;
     const float us = c.us * (float)((tiles + at_once - 1) / at_once);
     if (!best || us < least) {
@@ -545,6 +547,8 @@ static int launch_product(const Mx4Params& P, bool ybf, hipStream_t s) {
       least = us;
     }
   }
+  if (!best)
+    return fail(QMOE_ERR_UNSUPPORTED, "qgemm_mxfp4_mxfp4: R=%d N=%d: too many tiles", P.R, P.N);
   return best->launch(P, ybf, s);
 }
 

@@ -74,6 +74,7 @@ def test_product(L):
         assert g(**bad) == BAD, bad
     assert g(yd=2) == UNSUP
     assert g(N=(1 << 30) + 1) == UNSUP and g(R=(1 << 30) + 1) == UNSUP
+    assert g(N=1 << 20, R=1 << 24) == UNSUP           # 2^32 threads with every tile
 
 
 def test_the_binding_refuses_what_the_kernels_cannot_take():

@@ -250,6 +250,29 @@ def test_values_behind_the_last_row_stay():
             assert torch.equal(b[:R], t) and (b[R:] == 77).all()
 
 
+def test_offsets_past_32_bits():
+    """More than 2^32 values: the last rows come out as in a call on them alone."""
+    R, K, r = 2 ** 20 + 5, 4096, 7
+    last = to_gpu(_x((r, 2 * K), 23)).bfloat16()
+    w = to_gpu(np.abs(_x((K,), 24)))
+    x = torch.zeros((R, 2 * K), dtype=torch.bfloat16, device="cuda")
+    x[R - r:] = last
+    for fmt in FMTS:
+        got = qmoe.swiglu_act(fmt, x[:, :K], x[:, K:])
+        for a, b in zip(got, qmoe.swiglu_act(fmt, last[:, :K], last[:, K:])):
+            assert torch.equal(a[R - r:], b) and not a[:R - r].any()
+    x, last = x[:, :K].contiguous(), last[:, :K].contiguous()
+    for fmt in FMTS:
+        got = qmoe.norm_act(fmt, x, w, 1e-5, res=x)
+        for a, b in zip(got, qmoe.norm_act(fmt, last, w, 1e-5, res=last)):
+            assert torch.equal(a[R - r:], b) and not a[:R - r].any()
+    got, want = qmoe.quantize_act_mxfp4(x), qmoe.quantize_act_mxfp4(last)
+    for a, b in zip(got, want):
+        assert torch.equal(a[R - r:], b) and not a[:R - r].any()
+    y = qmoe.dequantize_act_mxfp4(*got)
+    assert torch.equal(y[R - r:], qmoe.dequantize_act_mxfp4(*want)) and not y[:R - r].any()
+
+
 def test_graph_replays_and_another_stream():
     R, K = 6, 2048
     x, res = to_gpu(_x((R, K), 17)), to_gpu(_x((R, K), 18))

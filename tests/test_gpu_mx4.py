@@ -113,6 +113,36 @@ def test_scales_at_any_address(R, N, K):
     assert torch.equal(want, qmoe.gemm_mxfp4_mxfp4(W, N, K, codes, scales))
 
 
+def _zeros_but_the_last(rows, last):
+    big = torch.zeros((rows,) + last.shape[1:], dtype=last.dtype, device="cuda")
+    big[rows - len(last):] = last
+    return big
+
+
+@pytest.mark.parametrize("R,N,K", [(2, 2 ** 29 + 80, 32), (2 ** 21 + 5, 48, 4096),
+                                   (2 ** 26 + 5, 80, 32)])
+def test_offsets_past_32_bits(R, N, K):
+    """Weights, activations and outputs whose offsets pass 2^32, all of it zero but
+    the last rows: exact sums there, as in a call on those rows alone, and zeros
+    elsewhere.  The widest W has more tiles of the smallest kind than a launch takes."""
+    rng = np.random.default_rng(11)
+    r, n = min(R, 40), min(N, 70)
+    q, wq = _codes(rng, r, K), _codes(rng, n, K)
+    e, we = (rng.integers(126, 129, (k, K // 32)).astype(np.uint8) for k in (r, n))
+    small = to_gpu(_w(wq, we, n, K)), to_gpu(act.pack_codes(q)), to_gpu(e)
+    want = qmoe.gemm_mxfp4_mxfp4(small[0], n, K, *small[1:], dtype=torch.bfloat16)
+    (c0, s0), (c1, s1) = qmoe.plane_offsets("mxfp4", n, K), qmoe.plane_offsets("mxfp4", N, K)
+    W = torch.zeros(qmoe.tensor_bytes("mxfp4", N, K), dtype=torch.uint8, device="cuda")
+    for row, o0, o1 in ((K // 2, c0, c1), (K // 32, s0, s1)):
+        W[o1 + (N - n) * row:o1 + N * row] = small[0][o0:o0 + n * row]
+    y = torch.full((R, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    qmoe.gemm_mxfp4_mxfp4(W, N, K, _zeros_but_the_last(R, small[1]),
+                          _zeros_but_the_last(R, small[2]), out=y)
+    assert torch.equal(y[R - r:, N - n:], want)
+    y[R - r:, N - n:] = 0
+    assert not y.any()
+
+
 def test_calls_on_two_streams_at_once():
     """No state is shared between calls: two streams at work together give what
     each gives alone."""
