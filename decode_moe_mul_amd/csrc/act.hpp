@@ -65,14 +65,17 @@ QMOE_D uint32_t block_max_bits(const float (&v)[8]) {
 }
 
 // Eight values over their block's scale as MX codes, saturating: clamping first
-// makes the conversions (nearest even) saturate, adding 0 turns a negative zero
-// into a positive one.  `top`: the type's largest value.
+// makes the conversions (nearest even) saturate.  `top`: the type's largest value.
+// The sign bit is v < 0, also where v over the scale is below fp32's smallest
+// number: of a multiply-add with 0 only the exact product is rounded, so that a
+// negative v stays negative (at least as -0) and a negative zero becomes +0.  A
+// product and a sum would make +0 of both.
 template <int OUT>
 QMOE_D uint2 mx_codes8(const float (&v)[8], float mul) {
   constexpr float top = OUT == kOutMx8 ? 448.f : 6.f;
   float t[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_fmed3f(v[i] * mul + 0.f, -top, top);
+  for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_fmed3f(fmaf(v[i], mul, 0.f), -top, top);
   if constexpr (OUT == kOutMx8) {
     int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
     w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w0, true);
@@ -125,7 +128,7 @@ QMOE_D void q8_codes8(const float (&v)[8], float d, uint32_t (&w)[2]) {
 // Store one octet of row-major [R, K] values at flat index `at` (a multiple
 // of 8) in the output type.  Every lane of the block's four calls this.
 //  * MX: codes of v / 2^E, E from the block's largest magnitude; scaling by a
-//    power of two is exact.
+//    power of two is exact but for values that vanish beside the block's largest.
 //  * int8: d = max * fp32(1 / 127), q = the quotient v / d (fp32) rounded half
 //    away from zero.
 template <int OUT>

@@ -53,6 +53,51 @@ def test_mxfp4_special_values():
     _same_act(qmoe.quantize_act_mxfp4(to_gpu(x)), act.quantize("mxfp4", x))
 
 
+def _signs():
+    """Blocks whose negative values are zero in their block's scale: below half
+    the element's smallest step, below fp32's smallest number, and -0, which is
+    no negative value."""
+    x = np.zeros((9, 64), np.float32)
+    x[0, :3] = [1e30, -1e-30, -1e-45]
+    x[1, :2] = [16, -1e-45]                       # -1e-45 / 2^E rounds to zero
+    x[2, :2] = [4, -1e-45]                        # and is itself here (E = 0)
+    x[3, :2] = [2.0 ** 100, -2.0 ** -60]
+    x[4, :4] = [3.4e38, -1.2e-38, 1.2e-38, -0.0]
+    x[5, :2] = [-1e30, 1e-30]
+    x[6, 32:] = -1e-45
+    x[6, 63] = 2.0 ** 127
+    x[7] = -np.float32(2.0) ** -110
+    x[7, ::32] = 2.0 ** 90
+    x[8] = [(-1) ** k * np.float32(2.0) ** (7 * k // 2 - 110) for k in range(64)]
+    return x
+
+
+def test_the_sign_of_values_that_vanish_in_their_block():
+    """Sign bit = (x < 0), as the weights' quantizer has it."""
+    x = _signs()
+    got = qmoe.quantize_act_mxfp4(to_gpu(x))
+    want = act.quantize("mxfp4", x)
+    assert want[0][0, 0] == 0x87                  # 1e30 saturates, -1e-30 is -0
+    _same_act(got, want)
+    W, off = qmoe.quantize("mxfp4", to_gpu(x)), qmoe.plane_offsets("mxfp4", *x.shape)
+    assert torch.equal(got[0].view(-1), W[:x.size // 2])
+    b = synth.bf16_round(x)
+    _same_act(qmoe.quantize_act_mxfp4(_dev(b, True)), act.quantize("mxfp4", b))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_the_sign_of_norm_and_swiglu_values_that_vanish_in_their_block(fmt):
+    for w in _signs():
+        x = np.ones((2, 64), np.float32)
+        x[1] = -1                                 # y = w and -w: the mean square is 1
+        y = act.rms_norm(x, w, 0.0)[0]
+        assert (y[0] == w).all()
+        _same_act(qmoe.norm_act(fmt, to_gpu(x), to_gpu(w), 0.0), act.quantize(fmt, y))
+    u = _signs() / np.float32(64)                 # SwiGLU with a gate of 64 is 64 up
+    g = np.full_like(u, 64)
+    _same_act(qmoe.swiglu_act(fmt, to_gpu(g), to_gpu(u)), act.quantize(fmt, act.swiglu(g, u)))
+
+
 @pytest.mark.parametrize("R,K", [(1, 32), (3, 96), (6, 2048), (5, 14336), (257, 160), (2, 65568)])
 @pytest.mark.parametrize("bf", [False, True], ids=["f32", "bf16"])
 def test_mxfp4_quantizer_and_read_back(R, K, bf):

@@ -23,6 +23,13 @@ def test_mxfp4_closed_forms():
     assert act.pack_codes(q)[0, :2].tolist() == [6 | 4 << 4, 12 | 6 << 4]
 
 
+def test_a_negative_value_that_vanishes_in_its_block_keeps_its_sign():
+    x = np.zeros((1, 32), np.float32)
+    x[0, :3] = [1e30, -1e-30, -0.0]
+    assert act.quantize("mxfp4", x)[0][0, :2].tolist() == [0x87, 0x00]
+    assert act.quantize("mxfp8", x)[0][0, :3].tolist() == [125, 128, 0]
+
+
 @pytest.mark.parametrize("fmt", ["q8", "mxfp8", "mxfp4"])
 @pytest.mark.parametrize("v", [np.nan, np.inf, -np.inf])
 def test_a_non_finite_block_is_marked_alone(fmt, v):
