@@ -107,6 +107,13 @@ QMOE_D void store_mx8(uint2 codes, int e, size_t at, void* out, void* scales) {
   if ((threadIdx.x & 3) == 0) ((uint8_t*)scales)[at >> 5] = (uint8_t)e;
 }
 
+// m / 127 rounded to nearest.  The fp64 product with 1 / 127 is within 2^-52 of the
+// quotient, and no quotient is nearer than 2^-32 to a border between two fp32
+// numbers: in halves of the quotient's last place, 127 times a border is an odd
+// number below 2^32, and m an even one.  (Norm 8192 x 7168 to int8 97.8 us; with an
+// fp32 division 98.9.)
+QMOE_D float over_127(float m) { return (float)((double)m * (1.0 / 127.0)); }
+
 // Eight int8 codes: the fp32 quotients v / d rounded half away from zero.  With
 // the reciprocal of d rounded to nearest (one division), a quotient is the
 // product, corrected once by its exact remainder: rounded to nearest by
@@ -129,8 +136,8 @@ QMOE_D void q8_codes8(const float (&v)[8], float d, uint32_t (&w)[2]) {
 // of 8) in the output type.  Every lane of the block's four calls this.
 //  * MX: codes of v / 2^E, E from the block's largest magnitude; scaling by a
 //    power of two is exact but for values that vanish beside the block's largest.
-//  * int8: d = max * fp32(1 / 127), q = the quotient v / d (fp32) rounded half
-//    away from zero.
+//  * int8: d = max / 127 (fp32), q = the quotient v / d (fp32) rounded half away
+//    from zero: qquantize_act_q8's rule.
 template <int OUT>
 QMOE_D void store_act8(const float (&v)[8], size_t at, void* out, void* scales) {
   if constexpr (OUT == kOutF32 || OUT == kOutBF16) {
@@ -140,7 +147,7 @@ QMOE_D void store_act8(const float (&v)[8], size_t at, void* out, void* scales) 
     const bool bad = m >= 0x7F800000u;
     const bool first = (threadIdx.x & 3) == 0;
     if constexpr (OUT == kOutQ8) {
-      const float d = __builtin_bit_cast(float, m) * (1.f / 127.f);
+      const float d = over_127(__builtin_bit_cast(float, m));
       uint32_t w[2] = {0, 0};
       q8_codes8(v, d, w);
       if (!(d > 0.f) || bad) w[0] = w[1] = 0;

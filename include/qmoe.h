@@ -387,8 +387,7 @@ int qgemm_q8_0_i8(const void *W, int N, int K, const int8_t *q, const float *d,
  * norm: qnorm_act_* -> product (gate and up) -> qswiglu_act_* -> product (down).
  *
  * Activation formats (K % 32 == 0, one scale per 32 values along K):
- *   q8    q [R, K] int8, d [R, K/32] fp32          as qquantize_act_q8, except
- *         that d = max|x| * fp32(1/127), one rounding more than max|x| / 127
+ *   q8    q [R, K] int8, d [R, K/32] fp32           as qquantize_act_q8
  *   mxfp8 codes [R, K] E4M3, scales [R, K/32] E8M0  as qquantize_act_mxfp8
  *   mxfp4 codes [R, K/2] E2M1 (low nibble first), scales [R, K/32] E8M0:
  *         E = floor(log2 max|x|) - 2, stored as E + 127 (at least 0; 0 for an

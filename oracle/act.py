@@ -16,6 +16,7 @@ zero codes, or d = NaN and q = 0.
 import numpy as np
 
 from . import formats as fm
+from . import int8
 from . import mx
 
 
@@ -64,12 +65,7 @@ def quantize(fmt, X):
     if fmt == "mxfp8":
         q, e = mx.quantize_mxfp8(X)
         return q, np.where(bad, 255, e).astype(np.uint8)
-    # as int8.quantize_act_q8, but d is max times the fp32 value of 1 / 127
-    x = X.reshape(X.shape[0], -1, 32)
-    d = np.abs(x).max(axis=-1) * (np.float32(1) / np.float32(127))
-    r = np.divide(x, d[..., None], out=np.zeros_like(x), where=d[..., None] > 0)
-    q = np.clip(fm.round_half_away(r.astype(np.float64)), -127, 127)
-    q = q.reshape(X.shape).astype(np.int8)
+    q, d = int8.quantize_act_q8(X)
     return q, np.where(bad, np.float32(np.nan), d)
 
 

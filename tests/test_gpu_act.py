@@ -193,6 +193,54 @@ def test_int8_codes_at_halves_and_with_tiny_scales():
     _same_act(qmoe.swiglu_act("q8", to_gpu(g), to_gpu(u)), act.quantize("q8", act.swiglu(g, u)))
 
 
+_SEPARATE = {"q8": qmoe.quantize_act_q8, "mxfp8": qmoe.quantize_act_mxfp8,
+             "mxfp4": qmoe.quantize_act_mxfp4}
+
+
+@pytest.mark.parametrize("R,K", [(1, 4096), (16, 7168), (500, 2080)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_norm_then_quantizer_is_norm_act(fmt, R, K):
+    """The fused call's codes and scales are those of the library's quantizer on
+    the norm's fp32 rows, to the last bit of an int8 scale."""
+    x, w = to_gpu(_x((R, K), 25)), to_gpu(1 + _x((1, K), 26, 0.1)[0])
+    want = _SEPARATE[fmt](qmoe.norm(x, w, 1e-5))
+    for a, b in zip(qmoe.norm_act(fmt, x, w, 1e-5), want):
+        assert torch.equal(a, b)
+
+
+def test_swiglu_then_int8_quantizer_is_swiglu_act():
+    g, u = _x((200, 2080), 27, 1.5), _x((200, 2080), 28, 1.5)
+    want = qmoe.quantize_act_q8(to_gpu(act.swiglu(g, u)))
+    for a, b in zip(qmoe.swiglu_act("q8", to_gpu(g), to_gpu(u)), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("big", [1.0, 3e38, 2e-36, 1e-38, 1e-43, 1e-44, 2e-45], ids=str)
+def test_int8_scale_of_any_size(big):
+    """Block maxima of every size, fp32 subnormals and scales of zero among them."""
+    x = (_x((4, 2048), 29) / 8).clip(-1, 1).astype(np.float32)
+    x[:, ::32] = np.linspace(1, 0.25, 64, dtype=np.float32)
+    x = (x * np.float32(big)).astype(np.float32)
+    w = x[0].copy()                               # y = w: the mean square is 1
+    ones = np.ones((1, 2048), np.float32)
+    got = qmoe.norm_act("q8", to_gpu(ones), to_gpu(w), 0.0)
+    want = act.quantize("q8", w[None])
+    _same_act(got, want)
+    for a, b in zip(got, qmoe.quantize_act_q8(to_gpu(w[None]))):
+        assert torch.equal(a, b)
+
+
+def test_int8_scale_of_every_significand():
+    """One block for each fp32 significand as its maximum."""
+    top = torch.arange(2 ** 23, dtype=torch.int32, device="cuda").add_(127 << 23).view(torch.float32)
+    u = torch.zeros((2 ** 23, 32), device="cuda")
+    u[:, 5] = top
+    want = qmoe.quantize_act_q8(u)
+    u.mul_(1 / 64)                                # SwiGLU with a gate of 64 is 64 up
+    q, d = qmoe.swiglu_act("q8", torch.full_like(u, 64), u)
+    assert torch.equal(d, want[1]) and torch.equal(q, want[0])
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_norm_of_x_added_to_itself_in_place(fmt):
     """x, res and res_out are one tensor: h = 2 x."""

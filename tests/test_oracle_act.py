@@ -98,3 +98,12 @@ def test_int8_is_within_one_step_of_the_int8_quantizer():
     assert (np.abs(d - d0) <= 2 * np.spacing(d0)).all() and (q[0] == 0).all() and (d[0] == 0).all()
     assert (np.abs(q.astype(int) - q0) <= 1).all() and (q != q0).mean() < 1e-3
     assert (np.abs(q.reshape(40, 10, 32)).max(-1)[1:] == 127).all()
+
+
+def test_int8_is_the_int8_quantizer():
+    from oracle import int8
+    x = np.random.default_rng(4).normal(0, 1, (400, 320)).astype(np.float32)
+    x[0], x[1] = 0, 1e-44
+    (q, d), (q0, d0) = act.quantize("q8", x), int8.quantize_act_q8(x)
+    assert (q == q0).all() and (d == d0).all()
+    assert (d == (np.abs(x.reshape(400, 10, 32)).max(-1) / np.float32(127))).all()
