@@ -481,6 +481,7 @@ _th = None           # torch, once a call has needed it, and two of its function
 _device = _stream_of = None
 _FLOAT = {}          # output and activation types -> dtype codes
 _ACT_TYPES = {}      # format -> (values per code, code type, scale type)
+_MOST = 2 ** 31 - 1  # sizes pass as C ints, of which ctypes keeps the low bits silently
 
 
 def _load_torch():
@@ -528,6 +529,8 @@ def _rows(x, what):
         raise QmoeError(f"{what} must be a contiguous float32 or bfloat16 CUDA tensor [R, K], "
                         f"not {x.dtype} {tuple(x.shape)} on {x.device}")
     R, K = x.shape
+    if R > _MOST or K > _MOST:
+        raise QmoeError(f"{what} [{R}, {K}]: sizes are below 2^31")
     return R, K, index, code
 
 
@@ -570,6 +573,8 @@ def _act_in(codes, scales, K):
         _refuse("codes", codes, (R, K // 2), u8, index)
     if not _is(scales, (R, K // 32), u8, index):
         _refuse("scales", scales, (R, K // 32), u8, index)
+    if R > _MOST or K > _MOST:
+        raise QmoeError(f"activations [{R}, {K}]: sizes are below 2^31")
     return R, index
 
 
@@ -651,6 +656,8 @@ def swiglu_act(fmt, gate, up, out=None):
         raise QmoeError("gate and up must be float32 or bfloat16 CUDA tensors [R, K] of one "
                         "type on one GPU")
     R, K = shape
+    if R > _MOST or K > _MOST:
+        raise QmoeError(f"gate and up [{R}, {K}]: sizes are below 2^31")
     ld = K
     if R > 0:
         (ld, one), (ld_up, one_up) = gate.stride(), up.stride()
@@ -669,6 +676,8 @@ def gemm_mxfp4_mxfp4(W, N, K, codes, scales, dtype=None, out=None):
     the MXFP4 activations; R from one decode row to a prefill chunk."""
     _th or _load_torch()
     R, index = _act_in(codes, scales, K)
+    if N > _MOST:
+        raise QmoeError(f"W [{N}, {K}]: sizes are below 2^31")
     if (N < 0 or W.dtype is not codes.dtype or W.get_device() != index or not W.is_contiguous()
             or W.numel() < -(-N * K // 512) * 256 + -(-N * K // 8192) * 256):
         raise QmoeError("W must be a packed MXFP4 [N, K] tensor on the activations' GPU")

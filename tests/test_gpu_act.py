@@ -366,6 +366,17 @@ def test_offsets_past_32_bits():
     assert torch.equal(y[R - r:], qmoe.dequantize_act_mxfp4(*want)) and not y[:R - r].any()
 
 
+def test_sizes_past_31_bits_are_refused():
+    """The C entries take rows as a 32-bit int: a larger count is an error of the
+    call, never its low bits.  The tensors are allocated only."""
+    R = 2 ** 32 + 5
+    x = torch.empty((R, 8), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(8, device="cuda")
+    out = torch.empty((R, 8), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(qmoe.QmoeError):
+        qmoe.norm(x, w, 1e-5, out=out)
+
+
 def test_graph_replays_and_another_stream():
     R, K = 6, 2048
     x, res = to_gpu(_x((R, K), 17)), to_gpu(_x((R, K), 18))

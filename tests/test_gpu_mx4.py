@@ -143,6 +143,19 @@ def test_offsets_past_32_bits(R, N, K):
     assert not y.any()
 
 
+@pytest.mark.parametrize("R,N,K", [(1, 2 ** 32 + 16, 32), (2 ** 32 + 1, 16, 32),
+                                   (1, 16, 2 ** 32 + 64)])
+def test_sizes_past_31_bits_are_refused(R, N, K):
+    """The C entry takes sizes as 32-bit ints: a larger one is an error of the call,
+    never its low bits.  The tensors are allocated only."""
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    W = torch.empty(qmoe.tensor_bytes("mxfp4", 1, 32) + (N * K // 2 + 511) // 256 * 256
+                    + N * K // 32, **u8)
+    with pytest.raises(qmoe.QmoeError):
+        qmoe.gemm_mxfp4_mxfp4(W, N, K, torch.empty((R, K // 2), **u8),
+                              torch.empty((R, K // 32), **u8), dtype=torch.bfloat16)
+
+
 def test_calls_on_two_streams_at_once():
     """No state is shared between calls: two streams at work together give what
     each gives alone."""
