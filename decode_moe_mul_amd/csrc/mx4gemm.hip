@@ -34,8 +34,8 @@ QMOE_D v4f_t mma4(uint4 a, uint32_t sa, uint4 b, uint32_t sb, v4f_t c) {
 }
 
 // ------------------------------------------------------ few rows ------
-// A block computes 16 weight rows x 16 activation rows with 16x16x128 ops; its
-// waves split K in turns of 512 values, and their sums meet in LDS in wave order.
+// A block computes 16 weight rows x all activation rows, 16 at most, with 16x16x128
+// ops; its waves split K in turns of 512 values, and their sums meet in LDS in wave order.
 // Operands go from memory to registers, a whole turn's loads together: with few
 // rows the call is a read of the weights, and what counts is how many of them
 // are on their way.
@@ -80,8 +80,8 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mxfp4_rows_kernel(Mx4Params P
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int nb = P.K >> 5, turns = (nb + 15) >> 4, full = nb >> 4;
-  const int n0 = blockIdx.x * 16, r0 = blockIdx.y * 16;
-  const size_t wrow = (size_t)min(n0 + i, P.N - 1) * nb, xrow = (size_t)min(r0 + i, P.R - 1) * nb;
+  const int n0 = blockIdx.x * 16;
+  const size_t wrow = (size_t)min(n0 + i, P.N - 1) * nb, xrow = (size_t)min(i, P.R - 1) * nb;
   v4f_t acc = v4f_t{0.f, 0.f, 0.f, 0.f};
   const auto turn = [&](auto tail, int u) {
     constexpr bool TAIL = decltype(tail)::value;
@@ -108,19 +108,19 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mxfp4_rows_kernel(Mx4Params P
     for (int j = 0; j < 4; ++j) acc[j] += v[j];
   }
   // lane 16 g + i: weight rows 4 g .. + 3 of activation row i
-  const int r = r0 + i, n = n0 + 4 * g;
-  if (r >= P.R) return;
+  const int n = n0 + 4 * g;
+  if (i >= P.R) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (n + j >= P.N) break;
-    const size_t at = (size_t)r * P.N + n + j;
+    const size_t at = (size_t)i * P.N + n + j;
     if constexpr (YBF) ((uint16_t*)P.y)[at] = (uint16_t)f32_to_bf16_bits(acc[j]);
     else ((float*)P.y)[at] = acc[j];
   }
 }
 
 static int launch_rows(const Mx4Params& P, bool ybf, hipStream_t s) {
-  const dim3 grid((unsigned)((P.N + 15) / 16), (unsigned)((P.R + 15) / 16));
+  const dim3 grid((unsigned)((P.N + 15) / 16));
   const int waves = std::min(kRowsWaves, (P.K / 32 + 15) / 16);
   if (ybf) return QMOE_LAUNCH("mxfp4_rows", mxfp4_rows_kernel<true>, grid, 64 * waves, 0, s, P);
   return QMOE_LAUNCH("mxfp4_rows", mxfp4_rows_kernel<false>, grid, 64 * waves, 0, s, P);
