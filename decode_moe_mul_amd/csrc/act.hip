@@ -76,8 +76,8 @@ QMOE_D float swiglu1(float g, float u) {
 }
 
 // The same in fp32, within kGluErr of it (relative) for finite results of
-// ordinary size and gate > -87: -gate log2 e = n + f with the product's error
-// carried along (f within 2^-25), the hardware's exp2 and reciprocal (an ulp,
+// ordinary size and gate > -87: Cody and Waite's reduction in base 2, -gate log2 e
+// = n + f with log2 e in two parts (f within 2^-25), the hardware's exp2 and reciprocal (an ulp,
 // 2^-23, each) and four roundings (2^-24 each) come to less than 2^-20.9.
 constexpr float kGluErr = 0x1p-20f;
 QMOE_D float swiglu1_near(float g, float u) {
@@ -102,8 +102,10 @@ struct GluParams {
 // bits: the fp32 value's neighbours at +-kGluErr have the same exponent and
 // code but for about one value in 10^5.  Where they differ, or the value is not
 // an ordinary one, the block's four lanes compute theirs in fp64; the result is
-// the fp64 one everywhere, in 30 us (4.5 TB/s; fp32 input 44).  int8 takes fp64,
-// 50 us: its scale carries every bit of the largest value.
+// the fp64 one everywhere, in 30 us (4.5 TB/s; fp32 input 44).  int8 takes fp64
+// throughout, 50-54 us (fp32 input 55-59): its scale carries every bit of the
+// block's largest value.  Of the other 31 only those near a half would need it;
+// no kernel here tells them apart.
 template <int OUT, bool XBF>
 __global__ __launch_bounds__(256) void swiglu_act_kernel(GluParams P) {
   const uint32_t o = blockIdx.x * 256 + threadIdx.x;

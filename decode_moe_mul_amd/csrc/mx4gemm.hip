@@ -43,8 +43,7 @@ QMOE_D v4f_t mma4(uint4 a, uint32_t sa, uint4 b, uint32_t sb, v4f_t c) {
 // Lane 16 g + i of step j takes block 4 j + g of the turn from row i, so that a
 // load reads 64 consecutive bytes of each of 16 rows.  (Four consecutive blocks
 // to a lane would put its scales into one word, but a load then touches four
-// times as many cache sectors: 16 x 14336 x 4096 takes 14.6 us instead of 12.7,
-// 1 x 4096 x 4096 4.6 instead of 4.3.)  The lane's scale of step j is byte g of
+// times as many cache sectors: 1 x 4096 x 4096 takes 4.6 us instead of 4.3.)  The lane's scale of step j is byte g of
 // the row's j-th scale word.
 struct Frag {  // one lane's part of a turn
   uint4 q[4];
@@ -132,9 +131,10 @@ static int launch_rows(const Mx4Params& P, bool ybf, hipStream_t s) {
 // code bytes of a row: four groups of ops, lane 32 h + i of group s taking block
 // 2 s + h of row i.
 //
-// A SIMD holds one wave (its sums fill half the registers), so whatever that
-// wave waits for, the matrix core waits for too.  Everything else is therefore
-// issued between matrix ops, in an order that the compiler keeps:
+// With the largest tile a SIMD holds one wave (its sums fill half the registers),
+// so whatever that wave waits for, the matrix core waits for too; the smaller ones
+// have two to four.  Everything else is therefore issued between matrix ops, in an
+// order that the compiler keeps:
 //  * codes go from memory to LDS without passing registers (16 bytes a lane,
 //    1 KB of LDS, 8 rows of 128 bytes, each a whole cache line: half lines
 //    doubled the requests to L2, which then set the pace), into one of two
@@ -529,6 +529,10 @@ static constexpr Choice choice(int slots, float us) {
 //   128 x 128, two teams 256 x 14336: 15.2; 64 x 128: 20.9; 256 x 256: 28.6
 //   128 x 128, two to a unit  2048 x 4096: 25.4; two teams: 30.0; 256 x 256: 30.2
 //   256 x 256  2048 x 14336: 70; 128 x 128: 86
+// The rule has no term for K.  Against the best of the six for R from 40 to 2048
+// and N from 2048 to 14336 its choice takes at most 5 % longer at K = 4096, 6 % at
+// 1024, 9 % at 14336 (700 x 4096: 40.2 and 36.9), and at 256, where the teams'
+// tiles are short of steps, 22 % (700 x 14336: 13.4 and 11.0).
 // A launch has fewer than 2^32 threads: a tile that would need more is passed over.
 static int launch_product(const Mx4Params& P, bool ybf, hipStream_t s) {
   const int cus = std::max(1, cu_count());

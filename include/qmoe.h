@@ -408,12 +408,15 @@ int qgemm_q8_0_i8(const void *W, int N, int K, const int8_t *q, const float *d,
  *     h = x + res   (fp32 sum, rounded to res_dtype, stored to res_out)
  *     h = x         when res is NULL (res_out must be NULL too)
  *     y = h * w / sqrt(mean_k h^2 + eps), rounded to fp32, then to y_dtype
- *   The sum, the root and the product are fp64, so y's fp32 value is the
- *   correctly rounded one (but for values within 2^-50 of a rounding border).
+ *   The sum, the root and the product are fp64, within 2^-47 of the definition,
+ *   so y's fp32 value is the correctly rounded one but for values that near a
+ *   rounding border.
  *   x [R, K] (x_dtype), res and res_out [R, K] (res_dtype, ignored without
  *   res), w [K] fp32, y [R, K].  res_out may be NULL, or res itself (in
  *   place).
- * qnorm_act_<fmt>: the activation quantizer of <fmt> applied to the fp32 y.
+ * qnorm_act_<fmt>: the activation quantizer of <fmt> applied to the fp32 y (to
+ *   the bit what qnorm, then that quantizer, gives; a non-finite block is marked
+ *   as above, which qquantize_act_q8 and qquantize_act_mxfp8 do not do).
  *   All pointers 16-byte aligned (mxfp scales: any; d: 4-byte).
  *   Limits: K <= 32768, K % 32 == 0 (qnorm: K % 8 == 0), eps >= 0.
  *
