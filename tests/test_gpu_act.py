@@ -127,6 +127,17 @@ def test_read_back_of_every_code_and_scale():
         assert_bitexact(y, act.dequantize_mxfp4(codes, e).astype(np.float32))
 
 
+def test_bf16_read_back_of_every_code_and_scale():
+    """bf16's subnormals, infinities and NaN among them: every finite value within
+    bf16's range is exact."""
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 2))
+    e = np.arange(256, dtype=np.uint8)[:, None]
+    got = qmoe.dequantize_act_mxfp4(to_gpu(act.pack_codes(codes)), to_gpu(e),
+                                    dtype=torch.bfloat16)
+    with np.errstate(over="ignore"):              # 2^128 and above are infinite in both
+        assert_bitexact(to_np(got.float()), act.dequantize_mxfp4(codes, e).astype(np.float32))
+
+
 # ---------------------------------------------------------------- norm --
 
 # one octet per thread, several waves a row, rows not a multiple of a block's,

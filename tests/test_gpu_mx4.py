@@ -85,6 +85,22 @@ def test_extreme_scales(R):
     assert_bitexact(to_np(y), ref)
 
 
+@pytest.mark.parametrize("R,N", [(1, 40), (20, 40), (300, 40), (2100, 8100)])
+@pytest.mark.parametrize("e", [57, 64, 70])
+def test_products_and_sums_below_the_normal_numbers(R, N, e):
+    """Scales of 2^-70 and less: every product is a multiple of 2^-142 and every sum
+    below 2^-142 2^24, so all of them are fp32 numbers, most of them subnormal."""
+    K = 256
+    rng = np.random.default_rng(R + e)
+    q, wq = _codes(rng, R, K), _codes(rng, N, K)
+    buf = _w(wq, np.full((N, K // 32), 57, np.uint8), N, K)
+    xe = np.full((R, K // 32), e, np.uint8)
+    y = qmoe.gemm_mxfp4_mxfp4(to_gpu(buf), N, K, to_gpu(act.pack_codes(q)), to_gpu(xe))
+    ref, bound = act.gemm_mxfp4(buf, N, K, q, xe)
+    assert bound.max() < 2.0 ** (e - 57 - 142 + 24)
+    assert_bitexact(to_np(y), ref)
+
+
 @pytest.mark.parametrize("R,N", [(1, 33), (16, 130), (70, 130), (300, 258)])
 @pytest.mark.parametrize("bf", [False, True], ids=["f32", "bf16"])
 def test_nothing_is_written_behind_the_last_row(R, N, bf):
