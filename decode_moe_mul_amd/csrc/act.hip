@@ -77,8 +77,9 @@ QMOE_D float swiglu1(float g, float u) {
 
 // The same in fp32, within kGluErr of it (relative) for finite results of
 // ordinary size and gate > -87: Cody and Waite's reduction in base 2, -gate log2 e
-// = n + f with log2 e in two parts (f within 2^-25), the hardware's exp2 and reciprocal (an ulp,
-// 2^-23, each) and four roundings (2^-24 each) come to less than 2^-20.9.
+// = n + f with log2 e in two parts (f within 2^-25), the hardware's exp2 and
+// reciprocal (an ulp, 2^-23, each) and four roundings (2^-24 each) come to less
+// than 2^-20.9.
 constexpr float kGluErr = 0x1p-20f;
 QMOE_D float swiglu1_near(float g, float u) {
   const float n = __builtin_rintf(g * -1.44269502f);

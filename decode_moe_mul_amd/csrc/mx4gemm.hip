@@ -43,8 +43,8 @@ QMOE_D v4f_t mma4(uint4 a, uint32_t sa, uint4 b, uint32_t sb, v4f_t c) {
 // Lane 16 g + i of step j takes block 4 j + g of the turn from row i, so that a
 // load reads 64 consecutive bytes of each of 16 rows.  (Four consecutive blocks
 // to a lane would put its scales into one word, but a load then touches four
-// times as many cache sectors: 1 x 4096 x 4096 takes 4.6 us instead of 4.3.)  The lane's scale of step j is byte g of
-// the row's j-th scale word.
+// times as many cache sectors: 1 x 4096 x 4096 takes 4.6 us instead of 4.3.)  The
+// lane's scale of step j is byte g of the row's j-th scale word.
 struct Frag {  // one lane's part of a turn
   uint4 q[4];
   uint32_t s[4];

@@ -12,9 +12,9 @@
 // takes at most 31 + 6 + 16 roundings (a thread's terms, the wave, the waves), the
 // mean and eps two, of which the root leaves half; with the root's own, the
 // reciprocal's and the last product's (h * w is exact) y is within 2^-47 of the
-// definition before it is rounded to fp32.  fp64 multiply-adds run at the rate of fp32 ones on this part, and the kernel
-// stays bound by memory: 8192 x 7168 bf16 to MXFP8, 413 MB, in 89-92 us (4.5 TB/s; a
-// 1 GiB copy moves 5.1).
+// definition before it is rounded to fp32.  fp64 multiply-adds run at the rate of
+// fp32 ones on this part, and the kernel stays bound by memory: 8192 x 7168 bf16 to
+// MXFP8, 413 MB, in 89-92 us (4.5 TB/s; a 1 GiB copy moves 5.1).
 #include <algorithm>
 
 #include "act.hpp"
