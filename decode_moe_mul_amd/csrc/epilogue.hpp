@@ -1,0 +1,331 @@
+// Internal header: what a product does with its sums before they leave: bias,
+// activation, the gated multiplication, residual.  All of it in fp32 on the fp32
+// sums, rounded once to the output's type.
+#pragma once
+#include <type_traits>
+#include <utility>
+
+#include "act.hpp"
+
+namespace qmoe {
+
+template <int I>
+using Int = std::integral_constant<int, I>;
+
+// f(0), f(1), .. with indices that are constants in f's own code: what they pick
+// among registers needs no loop to be unrolled first
+template <class F, int... I>
+QMOE_D void static_for_each(std::integer_sequence<int, I...>, F&& f) {
+  (f(Int<I>{}), ...);
+}
+template <int N, class F>
+QMOE_D void static_for(F&& f) {
+  static_for_each(std::make_integer_sequence<int, N>{}, f);
+}
+
+struct Epilogue {
+  const float* bias;   // [N] or NULL; of the gate where there are two products
+  const float* bias2;  // [N] or NULL, of up
+  const void* res;     // [R][N] or NULL; may be y itself (same type)
+  void* y;             // [R][N] values, or codes
+  void* scales;        // of a quantized output
+  int act;             // qmoe_act
+  int out;             // ActOut
+  int res_bf;          // res is bf16
+};
+
+// exp through the hardware's exp2: the product with log2 e is rounded, so the
+// relative error grows with |v|: |v| 2^-24 on top of exp2's own
+QMOE_D float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.4426950408889634f); }
+QMOE_D float recip(float v) { return __builtin_amdgcn_rcpf(v); }
+
+// Phi(-|v|) of the normal distribution: half of erfc(z), z = |v| / sqrt 2, as
+// t exp(-z^2) P(t), t = 1 / (1 + 0.4 z).  P of degree 8 is fitted to
+// exp(z^2) erfc(z) / t over all z >= 0 (minimax by reweighted least squares;
+// relative error 1.3e-7), so the tail keeps its relative precision, which
+// 1 + erf would lose.  15 instructions; a library erfc takes 40 with a branch.
+QMOE_D float normal_tail(float v) {
+  const float t = recip(fmaf(fabsf(v), 0.28284271247f, 1.f));
+  float p = 0.05025659129023552f;
+  p = fmaf(p, t, -0.18288160860538483f);
+  p = fmaf(p, t, 0.16905683279037476f);
+  p = fmaf(p, t, -0.005586383864283562f);
+  p = fmaf(p, t, 0.14142291247844696f);
+  p = fmaf(p, t, 0.16854381561279297f);
+  p = fmaf(p, t, 0.20784251391887665f);
+  p = fmaf(p, t, 0.22566960752010345f);
+  p = fmaf(p, t, 0.22567586600780487f);
+  return 0.5f * p * t * __builtin_amdgcn_exp2f(v * v * -0.72134752044f);
+}
+
+// The activation on E values; `act` is uniform over the launch, so the switch
+// is a scalar branch around straight-line code.  Infinities: silu, gelu and
+// gelu_tanh give NaN at -infinity, as their formulas do; NaN stays NaN.
+template <int E>
+QMOE_D void activate(int act, float (&v)[E]) {
+  switch (act) {
+    case QMOE_ACT_SILU:  // v / (1 + exp(-v)); exp's infinity gives -0
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] *= recip(1.f + exp_of(-v[k]));
+      break;
+    case QMOE_ACT_GELU:  // v Phi(v)
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float q = normal_tail(v[k]);
+        v[k] *= v[k] > 0.f ? 1.f - q : q;
+      }
+      break;
+    case QMOE_ACT_GELU_TANH:  // v / 2 (1 + tanh u) = v / (1 + exp(-2 u))
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float u = fmaf(v[k] * v[k] * v[k], 0.0713548162726f, v[k] * 1.5957691216057308f);
+        v[k] *= recip(1.f + exp_of(-u));
+      }
+      break;
+    case QMOE_ACT_RELU:
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = v[k] < 0.f ? 0.f : v[k];
+      break;
+    case QMOE_ACT_RELU2:
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = v[k] < 0.f ? 0.f : v[k] * v[k];
+      break;
+    default:
+      break;
+  }
+}
+
+QMOE_D float res_at(const Epilogue& e, size_t at) {
+  return e.res_bf ? bf16_bits_to_f32(((const uint16_t*)e.res)[at]) : ((const float*)e.res)[at];
+}
+QMOE_D void store_at(const Epilogue& e, size_t at, float v) {
+  if (e.out == kOutBF16) ((uint16_t*)e.y)[at] = (uint16_t)f32_to_bf16_bits(v);
+  else ((float*)e.y)[at] = v;
+}
+
+// Four consecutive columns n .. n + 3 of one row in a plain type, those that exist:
+// bias (`b`, one product's), activation and residual, where the launch has them.
+template <bool DONE>
+QMOE_D void leave4(const Epilogue& e, float (&v)[4], size_t row, int n, int N) {
+  if (n >= N) return;
+  const size_t at = row * N + n;
+  if constexpr (!DONE) {
+    if (e.bias)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += e.bias[min(n + j, N - 1)];
+    activate(e.act, v);
+    if (e.res)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += res_at(e, row * N + min(n + j, N - 1));
+  }
+  if (N % 4 == 0) {
+    if (e.out == kOutBF16)
+      *(uint2*)((uint16_t*)e.y + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    else
+      *(float4*)((float*)e.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < N) store_at(e, at + j, v[j]);
+  }
+}
+
+
+// A gated pair's four columns n .. n + 3: v = act(v + bias) * (up + bias2).
+QMOE_D void join4(const Epilogue& e, float (&v)[4], const float (&up)[4], int n, int N) {
+  if (e.bias)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += e.bias[min(n + j, N - 1)];
+  activate(e.act, v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] *= up[j] + (e.bias2 ? e.bias2[min(n + j, N - 1)] : 0.f);
+}
+
+// Columns n0 .. + 31 of activation row i, quantized: lane 16 g + i of the wave holds
+// columns 4 g .. + 3 (lo) and 16 + 4 g .. + 3 (hi).  Every lane calls this; N % 32 == 0.
+template <int OUT>
+QMOE_D void leave_block(const Epilogue& e, const float (&lo)[4], const float (&hi)[4], int i,
+                        int R, int n0, int N, int g) {
+  const float o[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  uint32_t m = 0;  // the largest magnitude's bits; a NaN's are above infinity's
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, __builtin_bit_cast(uint32_t, o[k]) & 0x7FFFFFFFu);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+  const bool bad = m >= 0x7F800000u;
+  if (i >= R) return;
+  const size_t at = (size_t)i * N + n0;
+  uint8_t* const y = (uint8_t*)e.y;
+  if constexpr (OUT == kOutQ8) {
+    const float d = over_127(__builtin_bit_cast(float, m));
+    uint32_t w[2] = {0, 0};
+    q8_codes8(o, d, w);
+    if (!(d > 0.f) || bad) w[0] = w[1] = 0;
+    *(uint32_t*)(y + at + 4 * g) = w[0];
+    *(uint32_t*)(y + at + 16 + 4 * g) = w[1];
+    if (g == 0) ((float*)e.scales)[at >> 5] = bad ? __builtin_nanf("") : d;
+  } else {
+    const int ex = mx_exponent<OUT>(m);
+    uint2 c = mx_codes8<OUT>(o, mx_over(ex));
+    if (bad) c = make_uint2(0, 0);
+    if constexpr (OUT == kOutMx8) {
+      *(uint32_t*)(y + at + 4 * g) = c.x;
+      *(uint32_t*)(y + at + 16 + 4 * g) = c.y;
+    } else {
+      *(uint16_t*)(y + at / 2 + 2 * g) = (uint16_t)c.x;
+      *(uint16_t*)(y + at / 2 + 8 + 2 * g) = (uint16_t)(c.x >> 16);
+    }
+    if (g == 0) ((uint8_t*)e.scales)[at >> 5] = (uint8_t)(bad ? 255 : ex);
+  }
+}
+
+// How the sums of a tile's wave leave: through LDS, 32 rows of the wave's COLS
+// columns at a time, so that a lane has eight consecutive columns of a row (of a
+// pair, where every 64 columns are 32 of the gate and 32 of up, eight of either).
+// Rows lie 8 words more than a multiple of 32 apart: the rows that one store of a
+// wave's sums touches are on different banks.  The region is the wave's own.
+//
+// The arithmetic stands in a loop that stays one: unrolled, every activation's code
+// would be there as often as the wave has pieces.
+constexpr int leave_pitch(int cols) { return cols + 8; }
+
+template <int COLS, bool GLU, int QUANT>  // QUANT: the ActOut of a quantized output
+struct Leave {
+  static constexpr int PITCH = leave_pitch(COLS), OC = GLU ? COLS / 2 : COLS;
+  static constexpr int LR = OC / 8, Z = LR / 2, STEP = 64 / LR;  // lanes to a row, pieces to a lane
+  struct Residual {
+    uint4 v[GLU ? 1 : Z][2];
+  };
+  const Epilogue& e;
+  float* p0;   // the lane's first piece
+  int R, N, c0, lrow;
+  float b1[8], b2[8];
+  bool wide, wide8;
+
+  QMOE_D Leave(const Epilogue& ep, float* region, int n0, int R_, int N_, int lane)
+      : e(ep), R(R_), N(N_) {
+    const int col = (lane % LR) * 8;
+    c0 = n0 + col;
+    lrow = lane / LR;
+    p0 = region + lrow * PITCH + (GLU ? (col >> 5 << 6) + (col & 31) : col);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int n = min(c0 + k, N - 1);
+      b1[k] = e.bias ? e.bias[n] : 0.f;
+      b2[k] = GLU && e.bias2 ? e.bias2[n] : 0.f;
+    }
+    wide = N % 4 == 0;
+    wide8 = N % 8 == 0;
+  }
+
+  // the residual of rows row0 .. + 31, all pieces at once: one wait for memory
+  QMOE_D Residual residual(int row0) const {
+    Residual r;
+    if (!GLU && e.res && wide) {
+#pragma unroll
+      for (int z = 0; z < (GLU ? 1 : Z); ++z) {
+        const size_t at = (size_t)min(row0 + lrow + z * STEP, R - 1) * N;
+        const int ca = min(c0, N - 4), cb = min(c0 + 4, N - 4);
+        if (!e.res_bf) {
+          r.v[z][0] = *(const uint4*)((const float*)e.res + at + ca);
+          r.v[z][1] = *(const uint4*)((const float*)e.res + at + cb);
+        } else if (wide8) {
+          r.v[z][0] = *(const uint4*)((const uint16_t*)e.res + at + min(c0, N - 8));
+        } else {
+          const uint2 u = *(const uint2*)((const uint16_t*)e.res + at + ca);
+          const uint2 v = *(const uint2*)((const uint16_t*)e.res + at + cb);
+          r.v[z][0] = make_uint4(u.x, u.y, v.x, v.y);
+        }
+      }
+    }
+    return r;
+  }
+
+  static QMOE_D void read8(const float* p, float (&v)[8]) {
+    const float4 lo = ((const float4*)p)[0], hi = ((const float4*)p)[1];
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  }
+
+  // the wave has written its sums of rows row0 .. + 31 to the region
+  QMOE_D void rows(int row0, const Residual& res) const {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (GLU || e.bias || e.act != QMOE_ACT_NONE) {
+#pragma unroll 1
+      for (int z = 0; z < Z; ++z) {  // a lane reads below what it writes here itself
+        float* const p = p0 + z * STEP * PITCH;
+        float v[8];
+        read8(p, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += b1[k];
+        activate(e.act, v);
+        if constexpr (GLU) {
+          float u[8];
+          read8(p + 32, u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] *= u[k] + b2[k];
+        }
+        ((float4*)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        ((float4*)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < Z; ++z) {
+      const int row = row0 + lrow + z * STEP;
+      if (row < R && c0 < N) {
+        const size_t at = (size_t)row * N + c0;
+        float v[8];
+        read8(p0 + z * STEP * PITCH, v);
+        if constexpr (!GLU)
+          if (e.res) add_residual(res.v[z], at, v);
+        store(at, v);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+
+  QMOE_D void add_residual(const uint4 (&r)[2], size_t at, float (&v)[8]) const {
+    if (!wide) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c0 + k < N) v[k] += res_at(e, at + k);
+    } else if (e.res_bf) {
+      const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] += bf16_bits_to_f32(w[k] & 0xFFFFu);
+        v[2 * k + 1] += __builtin_bit_cast(float, w[k] & 0xFFFF0000u);
+      }
+    } else {
+      const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += __builtin_bit_cast(float, w[k]);
+    }
+  }
+
+  QMOE_D void store(size_t at, const float (&v)[8]) const {
+    if (GLU && e.out > kOutBF16) {  // N % 32 == 0: a block's four lanes are all here
+      store_act8<QUANT>(v, at, e.y, e.scales);
+    } else if (!wide) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c0 + k < N) store_at(e, at + k, v[k]);
+    } else if (e.out == kOutF32) {
+      float* const y = (float*)e.y + at;
+      *(float4*)y = make_float4(v[0], v[1], v[2], v[3]);
+      if (c0 + 4 < N) *(float4*)(y + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint16_t* const y = (uint16_t*)e.y + at;
+      const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                 pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      if (wide8) {
+        *(uint4*)y = w;
+      } else {
+        *(uint2*)y = make_uint2(w.x, w.y);
+        if (c0 + 4 < N) *(uint2*)(y + 4) = make_uint2(w.z, w.w);
+      }
+    }
+  }
+};
+
+}  // namespace qmoe

@@ -1,0 +1,62 @@
+// The gated pair of products of MXFP4 weights with MXFP8 activations (qglu_mxfp8,
+// qglu_mxfp8_act).
+//
+//   v[r, n] = act( sum_k wg[n, k] x[r, k] + bg[n] ) * ( sum_k wu[n, k] x[r, k] + bu[n] )
+//
+// One pass over the activations for both weights; gate and up meet in the registers
+// that hold their sums and never go to memory.  v leaves in fp32, bf16 or as MXFP8
+// activations of the next product: the fp32 v, quantized.
+#include "mxcall.hpp"
+
+#pragma clang fp contract(off)
+
+namespace qmoe {
+
+template <int WR, int WC, int TM, int TN, int KS>
+using T8 = Tile<WR, WC, TM, TN, KS, true>;
+
+template <bool FINE>
+static int launch(const ProductCall& c, const MxProduct& P, hipStream_t s) {
+  const int cus = std::max(1, cu_count());
+  if (P.R <= 16 && P.N <= 32 * cus) {
+    if constexpr (!FINE)
+      if (P.e.out > kOutBF16) return launch_rows<true, true, 2>("mxfp8_glu_rows", P, s);
+    return launch_rows<true, true, 1, FINE>("mxfp8_glu_rows", P, s);
+  }
+  static constexpr Choice choices[] = {choice<T8<1, 2, 1, 2, 3>, true, FINE>(1, 10.f),
+                                       choice<T8<2, 2, 1, 2, 2>, true, FINE>(1, 14.f),
+                                       choice<T8<2, 2, 2, 2, 1>, true, FINE>(1, 22.f),
+                                       choice<T8<2, 2, 2, 4, 1>, true, FINE>(1, 40.f)};
+  return launch_choice(choices, c.who, "mxfp8_glu_tile", P, s);
+}
+
+static int run(const ProductCall& c, hipStream_t s) {
+  const int st = check_product(c);
+  if (st) return st == kNothing ? QMOE_OK : st;
+  const MxProduct P = mx_product(c);
+  return P.e.out == kOutF32 ? launch<true>(c, P, s) : launch<false>(c, P, s);
+}
+
+}  // namespace qmoe
+
+using namespace qmoe;
+
+extern "C" {
+
+int qglu_mxfp8(const void* Wg, const void* Wu, int N, int K, const uint8_t* codes,
+               const uint8_t* scales, int R, const float* bias_gate, const float* bias_up, int act,
+               void* y, int y_dtype, void* stream) {
+  const ProductCall c{"qglu_mxfp8", QMOE_MXFP4, Wg, Wu, true, N, K, codes, scales, R, bias_gate,
+                      bias_up, act, nullptr, 0, y, nullptr, plain_dtype(y_dtype)};
+  return run(c, (hipStream_t)stream);
+}
+
+int qglu_mxfp8_act(const void* Wg, const void* Wu, int N, int K, const uint8_t* codes,
+                   const uint8_t* scales, int R, const float* bias_gate, const float* bias_up,
+                   int act, uint8_t* out_codes, uint8_t* out_scales, void* stream) {
+  const ProductCall c{"qglu_mxfp8_act", QMOE_MXFP4, Wg, Wu, true, N, K, codes, scales, R,
+                      bias_gate, bias_up, act, nullptr, 0, out_codes, out_scales, kQuantized};
+  return run(c, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,48 @@
+// MXFP4 weights x MXFP8 activations with bias, activation and residual
+// (qlinear_mxfp8).
+//
+//   y[r, n] = act( sum_k w[n, k] x[r, k] + bias[n] ) + res[r, n]
+//
+// E2M1 codes against E4M3 codes, one E8M0 scale per 32 values along K on either
+// side, used as stored: every product of two codes is exact, the matrix op applies
+// both scales and accumulates in fp32.
+#include "mxcall.hpp"
+
+#pragma clang fp contract(off)
+
+namespace qmoe {
+
+template <int WR, int WC, int TM, int TN, int KS>
+using T8 = Tile<WR, WC, TM, TN, KS, true>;
+
+template <bool FINE>
+static int launch(const ProductCall& c, const MxProduct& P, hipStream_t s) {
+  const int cus = std::max(1, cu_count());
+  if (P.R <= 16 && P.N <= 32 * cus) return launch_rows<true, false, 1, FINE>("mxfp8_rows", P, s);
+  static constexpr Choice choices[] = {choice<T8<1, 2, 1, 1, 4>, false, FINE>(1, 8.f),
+                                       choice<T8<2, 2, 1, 1, 3>, false, FINE>(1, 11.f),
+                                       choice<T8<2, 2, 1, 2, 2>, false, FINE>(1, 14.f),
+                                       choice<T8<2, 2, 2, 2, 1>, false, FINE>(1, 22.f),
+                                       choice<T8<2, 2, 2, 4, 1>, false, FINE>(1, 40.f)};
+  return launch_choice(choices, c.who, "mxfp8_tile", P, s);
+}
+
+static int run(const ProductCall& c, hipStream_t s) {
+  const int st = check_product(c);
+  if (st) return st == kNothing ? QMOE_OK : st;
+  const MxProduct P = mx_product(c);
+  return P.e.out == kOutF32 ? launch<true>(c, P, s) : launch<false>(c, P, s);
+}
+
+}  // namespace qmoe
+
+using namespace qmoe;
+
+extern "C" int qlinear_mxfp8(const void* W, int N, int K, const uint8_t* codes,
+                             const uint8_t* scales, int R, const float* bias, int act,
+                             const void* res, int res_dtype, void* y, int y_dtype,
+                             void* stream) {
+  const ProductCall c{"qlinear_mxfp8", QMOE_MXFP4, W, nullptr, false, N, K, codes, scales, R,
+                      bias, nullptr, act, res, res_dtype, y, nullptr, plain_dtype(y_dtype)};
+  return run(c, (hipStream_t)stream);
+}

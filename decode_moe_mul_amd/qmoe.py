@@ -95,6 +95,16 @@ for _f in ("q8", "mxfp8", "mxfp4"):
     _SIGNATURES[f"qnorm_act_{_f}"] = (_I, _NORM_ARGS + [_VP, _VP, _VP])
     _SIGNATURES[f"qswiglu_act_{_f}"] = (_I, [_VP, _VP, _I, ctypes.c_longlong, _I, _I, _VP, _VP,
                                              _VP])
+_NORM_BLOCK_ARGS = [_VP, _I, _VP, ctypes.c_double, _VP, _I, _I, ctypes.c_double, _VP, _VP, _I,
+                    ctypes.c_double, _VP, ctypes.c_double, _I, _I]
+_SIGNATURES["qnorm_block"] = (_I, _NORM_BLOCK_ARGS + [_VP, _I, _VP])
+for _f in ("q8", "mxfp8", "mxfp4"):
+    _SIGNATURES[f"qnorm_block_act_{_f}"] = (_I, _NORM_BLOCK_ARGS + [_VP, _VP, _VP])
+    _SIGNATURES[f"qlinear_{_f}"] = (_I, [_VP, _I, _I, _VP, _VP, _I, _VP, _I, _VP, _I, _VP, _I,
+                                         _VP])
+    _SIGNATURES[f"qglu_{_f}"] = (_I, [_VP, _VP, _I, _I, _VP, _VP, _I, _VP, _VP, _I, _VP, _I, _VP])
+    _SIGNATURES[f"qglu_{_f}_act"] = (_I, [_VP, _VP, _I, _I, _VP, _VP, _I, _VP, _VP, _I, _VP, _VP,
+                                          _VP])
 _SIGNATURES["qgemv_batch"] = (_I, [_VP, _I, _VP])
 
 
@@ -685,6 +695,155 @@ def gemm_mxfp4_mxfp4(W, N, K, codes, scales, dtype=None, out=None):
     _launch("qgemm_mxfp4_mxfp4", index, W.data_ptr(), N, K, codes.data_ptr(), scales.data_ptr(),
             R, out.data_ptr(), yd)
     return out
+
+
+# -------------------------------------- the dense block, fused products --
+
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4, "relu2": 5}
+
+
+def _product_args(fmt, N, K, codes, scales, act, *weights):
+    """(R, GPU index, activation code) of a product's operands."""
+    kinds, code = _ACT_TYPES.get(fmt), ACTIVATIONS.get(act)
+    if kinds is None:
+        raise QmoeError(f"activation format {fmt!r} is not one of {ACT_FORMATS}")
+    if code is None:
+        raise QmoeError(f"activation {act!r} is not one of {tuple(ACTIVATIONS)}")
+    if K <= 0 or K % 32 or K > _MOST or not 0 <= N <= _MOST:
+        raise QmoeError(f"W [{N}, {K}]: N is at least 0, K a multiple of 32, both below 2^31")
+    per, ct, st = kinds
+    index, R = codes.get_device(), codes.shape[0] if codes.dim() else 0
+    if index < 0 or not _is(codes, (R, K // per), ct, index):
+        _refuse("codes", codes, (R, K // per), ct, index)
+    if not _is(scales, (R, K // 32), st, index):
+        _refuse("scales", scales, (R, K // 32), st, index)
+    if R > _MOST:
+        raise QmoeError(f"activations [{R}, {K}]: sizes are below 2^31")
+    # two planes, each from a 256-byte boundary on: int8 codes and fp16 scales, or
+    # 4-bit codes and one byte a scale
+    a, b = (256, 4096) if fmt == "q8" else (512, 8192)
+    need = (-(-N * K // a) - (-N * K // b)) * 256
+    for W in weights:
+        if (W.dtype is not _th.uint8 or W.get_device() != index or not W.is_contiguous()
+                or W.numel() < need):
+            raise QmoeError(f"weights must be a packed {'Q8_0' if fmt == 'q8' else 'MXFP4'} "
+                            f"[{N}, {K}] tensor on the activations' GPU")
+    return R, index, code
+
+
+def _bias(b, N, index, what):
+    if b is None:
+        return None
+    if not _is(b, (N,), _th.float32, index):
+        _refuse(what, b, (N,), _th.float32, index)
+    return b.data_ptr()
+
+
+def linear(fmt, W, N, K, codes, scales, bias=None, act=None, res=None, dtype=None, out=None):
+    """y [R, N] = act(x W^T + bias) + res (float32 unless dtype says bfloat16) of
+    activations x in format fmt ("q8", "mxfp8", "mxfp4": codes, scales) and packed
+    weights W [N, K], Q8_0 for "q8" and MXFP4 for the others; R from one decode
+    row to a prefill chunk.  bias: float32 [N]; act: one of ACTIVATIONS; res:
+    float32 or bfloat16 [R, N].  out may be res itself: the residual stream
+    updated in place."""
+    _th or _load_torch()
+    R, index, code = _product_args(fmt, N, K, codes, scales, act, W)
+    bias = _bias(bias, N, index, "bias")
+    rd, at = 0, None
+    if res is not None:
+        rd, at = _FLOAT.get(res.dtype), res.data_ptr()
+        if rd is None or not _is(res, (R, N), res.dtype, index):
+            _refuse("res", res, (R, N), "float32 or bfloat16", index)
+    out, yd = _float_out(out, dtype, codes, (R, N), index)
+    _launch("qlinear_" + fmt, index, W.data_ptr(), N, K, codes.data_ptr(), scales.data_ptr(), R,
+            bias, code, at, rd, out.data_ptr(), yd)
+    return out
+
+
+def glu(fmt, Wg, Wu, N, K, codes, scales, act="silu", bias_gate=None, bias_up=None, dtype=None,
+        out=None):
+    """y [R, N] = act(x Wg^T + bias_gate) * (x Wu^T + bias_up), operands as linear
+    takes them, in float32 unless dtype says bfloat16."""
+    _th or _load_torch()
+    R, index, code = _product_args(fmt, N, K, codes, scales, act, Wg, Wu)
+    bg, bu = _bias(bias_gate, N, index, "bias_gate"), _bias(bias_up, N, index, "bias_up")
+    out, yd = _float_out(out, dtype, codes, (R, N), index)
+    _launch("qglu_" + fmt, index, Wg.data_ptr(), Wu.data_ptr(), N, K, codes.data_ptr(),
+            scales.data_ptr(), R, bg, bu, code, out.data_ptr(), yd)
+    return out
+
+
+def glu_act(fmt, Wg, Wu, N, K, codes, scales, act="silu", bias_gate=None, bias_up=None, out=None):
+    """glu's float32 rows as activations (codes, scales) of the next product, in
+    the same format fmt."""
+    _th or _load_torch()
+    R, index, code = _product_args(fmt, N, K, codes, scales, act, Wg, Wu)
+    bg, bu = _bias(bias_gate, N, index, "bias_gate"), _bias(bias_up, N, index, "bias_up")
+    oc, os_ = _act_out(fmt, codes, R, N, index, out)
+    _launch("qglu_" + fmt + "_act", index, Wg.data_ptr(), Wu.data_ptr(), N, K, codes.data_ptr(),
+            scales.data_ptr(), R, bg, bu, code, oc.data_ptr(), os_.data_ptr())
+    return oc, os_
+
+
+def _norm_block_args(x, res, w, eps, w_post, eps_post, gate, scale, res_scale, res_out):
+    R, K, index, xd = _rows(x, "x")
+    f32 = _th.float32
+    if not _is(w, (K,), f32, index):
+        _refuse("w", w, (K,), f32, index)
+    post = None
+    if w_post is not None:
+        if not _is(w_post, (K,), f32, index):
+            _refuse("w_post", w_post, (K,), f32, index)
+        post = w_post.data_ptr()
+    rd, shape = _FLOAT.get(res.dtype), x.shape
+    if rd is None or not _is(res, shape, res.dtype, index):
+        _refuse("res", res, shape, "float32 or bfloat16", index)
+    if res_out is None:
+        res_out = _th.empty_like(res)
+    elif res_out is not res and not _is(res_out, shape, res.dtype, index):
+        _refuse("res_out", res_out, shape, res.dtype, index)
+    gd, gates, gp = 0, 1, None
+    if gate is not None:
+        gates = gate.shape[0] if gate.dim() == 2 else 1
+        gd = _FLOAT.get(gate.dtype)
+        want = (gates, K) if gate.dim() == 2 else (K,)
+        if gd is None or not _is(gate, want, gate.dtype, index):
+            _refuse("gate", gate, want, "float32 or bfloat16", index)
+        gates = gates if R else 1
+        if gates < 1 or R % gates:
+            raise QmoeError(f"gate [{gates}, {K}]: its rows must divide x's {R}")
+        gp = gate.data_ptr()
+    return index, R, K, res_out, (
+        x.data_ptr(), xd, post, eps if eps_post is None else eps_post, gp, gd, gates, scale,
+        res.data_ptr(), res_out.data_ptr(), rd, res_scale, w.data_ptr(), eps, R, K)
+
+
+def norm_block(x, res, w, eps, w_post=None, eps_post=None, gate=None, scale=1.0, res_scale=1.0,
+               res_out=None, dtype=None, out=None):
+    """The norms around a block: h = res_scale * res + scale * gate * z, where z is
+    the RMS norm of the block's output x [R, K] with weights w_post (x itself
+    without them), and y, the RMS norm of h with weights w.  eps_post is eps
+    unless given.  gate: float32 or bfloat16, [K], or [G, K] for R / G rows each.
+    Returns (y, h): y float32 unless dtype says bfloat16, h in res' type, to
+    res_out (a new tensor unless given; res itself for an update in place)."""
+    _th or _load_torch()
+    index, R, K, h, args = _norm_block_args(x, res, w, eps, w_post, eps_post, gate, scale,
+                                            res_scale, res_out)
+    out, yd = _float_out(out, dtype, x, (R, K), index)
+    _launch("qnorm_block", index, *args, out.data_ptr(), yd)
+    return out, h
+
+
+def norm_block_act(fmt, x, res, w, eps, w_post=None, eps_post=None, gate=None, scale=1.0,
+                   res_scale=1.0, res_out=None, out=None):
+    """norm_block's float32 y in activation format fmt ("q8", "mxfp8", "mxfp4"):
+    (codes, scales, h)."""
+    _th or _load_torch()
+    index, R, K, h, args = _norm_block_args(x, res, w, eps, w_post, eps_post, gate, scale,
+                                            res_scale, res_out)
+    codes, scales = _act_out(fmt, x, R, K, index, out)
+    _launch("qnorm_block_act_" + fmt, index, *args, codes.data_ptr(), scales.data_ptr())
+    return codes, scales, h
 
 
 def layer_decode_workspace(T, H, E, F, k, n_shared=0, device="cuda"):

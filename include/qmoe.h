@@ -99,6 +99,16 @@ typedef enum {
 
 typedef enum { QMOE_F32 = 0, QMOE_BF16 = 1 } qmoe_dtype;
 
+/* Activation functions of the products with an epilogue. */
+typedef enum {
+  QMOE_ACT_NONE = 0,
+  QMOE_ACT_SILU = 1,      /* v / (1 + exp(-v))                                  */
+  QMOE_ACT_GELU = 2,      /* v Phi(v), Phi the normal distribution              */
+  QMOE_ACT_GELU_TANH = 3, /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))      */
+  QMOE_ACT_RELU = 4,      /* max(v, 0)                                          */
+  QMOE_ACT_RELU2 = 5      /* max(v, 0)^2                                        */
+} qmoe_act;
+
 /* ---------------------------------------------------------------- meta -- */
 int qmoe_abi_version(void);
 const char *qmoe_status_string(int status);
@@ -456,6 +466,97 @@ int qswiglu_act_mxfp4(const void *gate, const void *up, int x_dtype, long long l
 int qgemm_mxfp4_mxfp4(const void *W, int N, int K, const uint8_t *codes,
                       const uint8_t *scales, int R, void *y, int y_dtype,
                       void *stream);
+
+/* -------------------- the dense block's products and norms, fused ----
+ * What stands between two products of a dense layer, in the products' and the
+ * norms' own launches: qnorm_block_act_<fmt> -> qglu_<fmt>_act (gate, up,
+ * activation, product, quantized) -> qlinear_<fmt> (down) -> the next
+ * qnorm_block_act_<fmt>, or qlinear_<fmt> with the residual where a layer has
+ * no norm behind its blocks.
+ *
+ * <fmt> names both operands (K % 32 == 0, K <= 65536):
+ *   q8    int8 activations q [R, K], d [R, K/32] fp32; weights Q8_0
+ *   mxfp8 codes [R, K] E4M3, scales [R, K/32] E8M0;   weights MXFP4
+ *   mxfp4 codes [R, K/2] E2M1, scales [R, K/32] E8M0; weights MXFP4
+ * W, Wg, Wu [N, K] in qmoe layout, 256-byte aligned; activations as the
+ * quantizers, qnorm_act_*, qnorm_block_act_*, qswiglu_act_* and qglu_*_act
+ * write them, codes 16-byte aligned (d: 4, E8M0 scales: any).  Products of codes
+ * are exact, of q8 the sums over a 32-value block too; sums are fp32 from there.
+ * (mxfp8 with a result in bf16 or in codes: of eight consecutive products, what
+ * lies more than 13 binary places below the largest is dropped, 4.5e-6 of a sum of
+ * normal values and at most 2^-10 sum |w x|; with a result in fp32 nothing is.)
+ * The kernel that R and N call for may sum in another order, so a row's last
+ * bits can depend on R.
+ *
+ * qlinear_<fmt>: y [R, N] (y_dtype) = act( sum_k w[n, k] x[r, k] + bias[n] )
+ *                                     + res[r, n]
+ *   bias [N] fp32 (4-byte aligned) or NULL; res [R, N] (res_dtype, ignored
+ *   without res) or NULL, and it may be y itself where the types are the same.
+ * qglu_<fmt>: y [R, N] (y_dtype) =
+ *     act( sum_k wg[n, k] x[r, k] + bias_gate[n] )
+ *     * ( sum_k wu[n, k] x[r, k] + bias_up[n] )
+ *   bias_gate, bias_up [N] fp32 or NULL.
+ * qglu_<fmt>_act: the activation quantizer of <fmt> applied to qglu's fp32 y
+ *   (N % 32 == 0; scales at any address, out_d 4-byte aligned).  A block with
+ *   a NaN or an infinity is marked as in the section above.
+ *   act is a qmoe_act.  Everything after the sums is fp32, with exponentials
+ *   and reciprocals of the hardware: an activation of v is within 2^-20
+ *   (1 + v^2 / 4) (relative) or 2^-118 of its formula.  silu, gelu and gelu_tanh
+ *   of -infinity are NaN.
+ *   y and res 16-byte aligned.  R, N <= 2^30.
+ *
+ * qnorm_block: the norms around a block, its gate and the residual's scale:
+ *     z = x * w_post / sqrt(mean_k x^2 + eps_post)   (z = x without w_post)
+ *     h = res_scale * res + scale * gate * z         (rounded to fp32, then to
+ *                                                     res_dtype; to res_out)
+ *     y = h * w / sqrt(mean_k h^2 + eps), rounded to fp32, then to y_dtype
+ *   Each line before its rounding is taken in fp64: h is the correctly rounded
+ *   value, and y's fp32 value as well, but for values that near a rounding border.
+ *   x [R, K] (x_dtype) is the block's output, res [R, K] (res_dtype) the stream
+ *   it joins; res_out may be NULL, or res itself (in place).  w_post and w [K]
+ *   fp32; w_post may be NULL (eps_post is ignored then).  gate [gate_rows, K]
+ *   (gate_dtype) or NULL (1): gate_rows divides R, and row r takes gate row
+ *   r / (R / gate_rows): 1 for a gate per channel, R for one per row, or one
+ *   for each of gate_rows sequences of equal length.
+ * qnorm_block_act_<fmt>: the activation quantizer of <fmt> applied to the fp32 y
+ *   (a non-finite block is marked).
+ *   All pointers 16-byte aligned (mxfp scales: any; d: 4-byte).
+ *   Limits: K <= 32768, K % 32 == 0 (qnorm_block: K % 8 == 0), eps >= 0,
+ *   eps_post >= 0.
+ * No output may overlap an input or another output, but for y == res and
+ *   res_out == res.
+ * Errors: INVALID_ARG for sizes, null pointers, misalignment and a y that is res
+ *   in another type; UNSUPPORTED for unknown dtypes and activations and for sizes
+ *   beyond a limit.                                                            */
+#define QMOE_DECLARE_PRODUCTS(F, CODES, SCALES)                                 \
+  int qlinear_##F(const void *W, int N, int K, const CODES *codes,              \
+                  const SCALES *scales, int R, const float *bias, int act,      \
+                  const void *res, int res_dtype, void *y, int y_dtype,         \
+                  void *stream);                                                \
+  int qglu_##F(const void *Wg, const void *Wu, int N, int K,                    \
+               const CODES *codes, const SCALES *scales, int R,                 \
+               const float *bias_gate, const float *bias_up, int act, void *y,  \
+               int y_dtype, void *stream);                                      \
+  int qglu_##F##_act(const void *Wg, const void *Wu, int N, int K,              \
+                     const CODES *codes, const SCALES *scales, int R,           \
+                     const float *bias_gate, const float *bias_up, int act,     \
+                     CODES *out_codes, SCALES *out_scales, void *stream);
+QMOE_DECLARE_PRODUCTS(q8, int8_t, float)
+QMOE_DECLARE_PRODUCTS(mxfp8, uint8_t, uint8_t)
+QMOE_DECLARE_PRODUCTS(mxfp4, uint8_t, uint8_t)
+#undef QMOE_DECLARE_PRODUCTS
+#define QMOE_NORM_BLOCK_ARGS                                                    \
+  const void *x, int x_dtype, const float *w_post, double eps_post,             \
+      const void *gate, int gate_dtype, int gate_rows, double scale,            \
+      const void *res, void *res_out, int res_dtype, double res_scale,          \
+      const float *w, double eps, int R, int K
+int qnorm_block(QMOE_NORM_BLOCK_ARGS, void *y, int y_dtype, void *stream);
+int qnorm_block_act_q8(QMOE_NORM_BLOCK_ARGS, int8_t *q, float *d, void *stream);
+int qnorm_block_act_mxfp8(QMOE_NORM_BLOCK_ARGS, uint8_t *codes, uint8_t *scales,
+                          void *stream);
+int qnorm_block_act_mxfp4(QMOE_NORM_BLOCK_ARGS, uint8_t *codes, uint8_t *scales,
+                          void *stream);
+#undef QMOE_NORM_BLOCK_ARGS
 
 /* moe_layer_decode: the whole routed-expert layer of a decode step in one
  * launch ([P2] "瓶颈分析": router top-k over the experts, the selected
