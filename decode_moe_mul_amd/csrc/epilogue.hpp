@@ -185,60 +185,38 @@ QMOE_D void leave_block(const Epilogue& e, const float (&lo)[4], const float (&h
 // Rows lie 8 words more than a multiple of 32 apart: the rows that one store of a
 // wave's sums touches are on different banks.  The region is the wave's own.
 //
-// The arithmetic stands in a loop that stays one: unrolled, every activation's code
-// would be there as often as the wave has pieces.
+// A tile's code here runs once, so what it costs is its fetching: the arithmetic
+// stands in a loop that stays one (unrolled, every activation's code would be there
+// as often as the wave has pieces), and each way of storing is a loop of its own, so
+// that a tile runs through a short straight piece of them (with the choice inside the
+// loop the largest tile's 17000 instructions took a call of 70 us to 95).
 constexpr int leave_pitch(int cols) { return cols + 8; }
 
 template <int COLS, bool GLU, int QUANT>  // QUANT: the ActOut of a quantized output
 struct Leave {
   static constexpr int PITCH = leave_pitch(COLS), OC = GLU ? COLS / 2 : COLS;
   static constexpr int LR = OC / 8, Z = LR / 2, STEP = 64 / LR;  // lanes to a row, pieces to a lane
-  struct Residual {
-    uint4 v[GLU ? 1 : Z][2];
-  };
+  enum Res { kNone, kBF16, kF32 };
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   const Epilogue& e;
+  float* region;
   float* p0;   // the lane's first piece
-  int R, N, c0, lrow;
+  int R, N, n0, lane;
   float b1[8], b2[8];
-  bool wide, wide8;
 
-  QMOE_D Leave(const Epilogue& ep, float* region, int n0, int R_, int N_, int lane)
-      : e(ep), R(R_), N(N_) {
+  static QMOE_D int lds_col(int col) { return GLU ? (col >> 5 << 6) + (col & 31) : col; }
+
+  QMOE_D Leave(const Epilogue& ep, float* reg, int first, int R_, int N_, int lane_)
+      : e(ep), region(reg), R(R_), N(N_), n0(first), lane(lane_) {
     const int col = (lane % LR) * 8;
-    c0 = n0 + col;
-    lrow = lane / LR;
-    p0 = region + lrow * PITCH + (GLU ? (col >> 5 << 6) + (col & 31) : col);
+    p0 = region + lane / LR * PITCH + lds_col(col);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int n = min(c0 + k, N - 1);
+      const int n = min(n0 + col + k, N - 1);
       b1[k] = e.bias ? e.bias[n] : 0.f;
       b2[k] = GLU && e.bias2 ? e.bias2[n] : 0.f;
     }
-    wide = N % 4 == 0;
-    wide8 = N % 8 == 0;
-  }
-
-  // the residual of rows row0 .. + 31, all pieces at once: one wait for memory
-  QMOE_D Residual residual(int row0) const {
-    Residual r;
-    if (!GLU && e.res && wide) {
-#pragma unroll
-      for (int z = 0; z < (GLU ? 1 : Z); ++z) {
-        const size_t at = (size_t)min(row0 + lrow + z * STEP, R - 1) * N;
-        const int ca = min(c0, N - 4), cb = min(c0 + 4, N - 4);
-        if (!e.res_bf) {
-          r.v[z][0] = *(const uint4*)((const float*)e.res + at + ca);
-          r.v[z][1] = *(const uint4*)((const float*)e.res + at + cb);
-        } else if (wide8) {
-          r.v[z][0] = *(const uint4*)((const uint16_t*)e.res + at + min(c0, N - 8));
-        } else {
-          const uint2 u = *(const uint2*)((const uint16_t*)e.res + at + ca);
-          const uint2 v = *(const uint2*)((const uint16_t*)e.res + at + cb);
-          r.v[z][0] = make_uint4(u.x, u.y, v.x, v.y);
-        }
-      }
-    }
-    return r;
   }
 
   static QMOE_D void read8(const float* p, float (&v)[8]) {
@@ -247,84 +225,158 @@ struct Leave {
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
   }
 
-  // the wave has written its sums of rows row0 .. + 31 to the region
-  QMOE_D void rows(int row0, const Residual& res) const {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (GLU || e.bias || e.act != QMOE_ACT_NONE) {
-#pragma unroll 1
-      for (int z = 0; z < Z; ++z) {  // a lane reads below what it writes here itself
-        float* const p = p0 + z * STEP * PITCH;
-        float v[8];
-        read8(p, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += b1[k];
-        activate(e.act, v);
-        if constexpr (GLU) {
-          float u[8];
-          read8(p + 32, u);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] *= u[k] + b2[k];
+  // Plain types: piece z of a lane is columns E l .. + E - 1 of a row, 16 bytes of y.
+  // N % E == 0, so that a piece is there or not as one, and aligned.
+  template <int OUT>
+  struct Piece {
+    static constexpr int E = OUT == kOutBF16 ? 8 : 4, LR = OC / E, Z = 32 * LR / 64;
+  };
+  template <Res RES, int OUT>
+  struct Residual {  // of a lane's pieces of 32 rows, four columns to an element
+    static constexpr int H = Piece<OUT>::E / 4;
+    typename std::conditional<RES == kBF16, u32x2, u32x4>::type v[RES == kNone ? 1 : Piece<OUT>::Z * H];
+  };
+  // the residual of rows row0 .. + 31, all pieces at once: one wait for memory
+  template <Res RES, int OUT>
+  QMOE_D void load(int row0, Residual<RES, OUT>& r) const {
+    using P = Piece<OUT>;
+    if constexpr (RES != kNone) {
+      const int c = min(n0 + lane % P::LR * P::E, N - P::E);
+      static_for<P::Z>([&](auto z) {
+        const size_t at = (size_t)min(row0 + lane / P::LR + z * (64 / P::LR), R - 1) * N + c;
+        if constexpr (RES == kBF16 && P::E == 8) {
+          const u32x4 q = *(const u32x4*)((const uint16_t*)e.res + at);
+          r.v[2 * z] = u32x2{q[0], q[1]};
+          r.v[2 * z + 1] = u32x2{q[2], q[3]};
+        } else if constexpr (RES == kBF16) {
+          r.v[z] = *(const u32x2*)((const uint16_t*)e.res + at);
+        } else {
+          const u32x4* p = (const u32x4*)((const float*)e.res + at);
+          r.v[P::E / 4 * z] = p[0];
+          if constexpr (P::E == 8) r.v[2 * z + 1] = p[1];
         }
-        ((float4*)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        ((float4*)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      }
+      });
     }
+  }
+  template <Res RES, int OUT>
+  QMOE_D void store_rows(int row0, const Residual<RES, OUT>& res) const {
+    using P = Piece<OUT>;
+    const int col = lane % P::LR * P::E;
+    static_for<P::Z>([&](auto z) {
+      const int lrow = lane / P::LR + z * (64 / P::LR), row = row0 + lrow;
+      if (row < R && n0 + col < N) {
+        const float4* p = (const float4*)(region + lrow * PITCH + lds_col(col));
+        float v[P::E];
+        static_for<P::E / 4>([&](auto h) {
+          const float4 f = p[h];
+          v[4 * h] = f.x; v[4 * h + 1] = f.y; v[4 * h + 2] = f.z; v[4 * h + 3] = f.w;
+          const auto r = res.v[RES == kNone ? 0 : P::E / 4 * z + h];
 #pragma unroll
-    for (int z = 0; z < Z; ++z) {
-      const int row = row0 + lrow + z * STEP;
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (RES == kBF16) {
+              const uint32_t w = r[k / 2];
+              v[4 * h + k] += bf16_bits_to_f32(k & 1 ? w >> 16 : w & 0xFFFFu);
+            } else if constexpr (RES == kF32) {
+              v[4 * h + k] += __builtin_bit_cast(float, (uint32_t)r[k]);
+            }
+          }
+        });
+        const size_t at = (size_t)row * N + n0 + col;
+        if constexpr (OUT == kOutBF16)
+          *(uint4*)((uint16_t*)e.y + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                      pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        else
+          *(float4*)((float*)e.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    });
+  }
+  // Quantized (N % 32 == 0): eight columns to a lane, and a block's four lanes are
+  // there or not together.
+  QMOE_D void store_codes(int row0) const {
+    const int c0 = n0 + (lane % LR) * 8;
+    static_for<Z>([&](auto z) {
+      const int row = row0 + lane / LR + z * STEP;
       if (row < R && c0 < N) {
-        const size_t at = (size_t)row * N + c0;
         float v[8];
         read8(p0 + z * STEP * PITCH, v);
-        if constexpr (!GLU)
-          if (e.res) add_residual(res.v[z], at, v);
-        store(at, v);
+        store_act8<QUANT>(v, (size_t)row * N + c0, e.y, e.scales);
       }
+    });
+  }
+  // Any width: consecutive lanes take consecutive columns.
+  template <Res RES, int OUT>
+  QMOE_D void store_each(int row0) const {
+#pragma unroll 4
+    for (int o = lane; o < 32 * OC; o += 64) {
+      const int row = o / OC, col = o % OC;
+      if (row0 + row < R && n0 + col < N) {
+        const size_t at = (size_t)(row0 + row) * N + n0 + col;
+        float v = region[row * PITCH + lds_col(col)];
+        if constexpr (RES == kBF16) v += bf16_bits_to_f32(((const uint16_t*)e.res)[at]);
+        if constexpr (RES == kF32) v += ((const float*)e.res)[at];
+        if constexpr (OUT == kOutBF16) ((uint16_t*)e.y)[at] = (uint16_t)f32_to_bf16_bits(v);
+        else ((float*)e.y)[at] = v;
+      }
+    }
+  }
+
+  QMOE_D void math() const {
+    if (!GLU && !e.bias && e.act == QMOE_ACT_NONE) return;
+#pragma unroll 1
+    for (int z = 0; z < Z; ++z) {
+      float* const p = p0 + z * STEP * PITCH;
+      float v[8];
+      read8(p, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += b1[k];
+      activate(e.act, v);
+      if constexpr (GLU) {
+        float u[8];
+        read8(p + 32, u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= u[k] + b2[k];
+      }
+      ((float4*)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      ((float4*)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 
-  QMOE_D void add_residual(const uint4 (&r)[2], size_t at, float (&v)[8]) const {
-    if (!wide) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c0 + k < N) v[k] += res_at(e, at + k);
-    } else if (e.res_bf) {
-      const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] += bf16_bits_to_f32(w[k] & 0xFFFFu);
-        v[2 * k + 1] += __builtin_bit_cast(float, w[k] & 0xFFFF0000u);
-      }
-    } else {
-      const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += __builtin_bit_cast(float, w[k]);
+  // One way of storing: rows row0 + 32 m .. + 31 for m < M; write(m) puts the wave's
+  // sums of those rows into the region, which is this wave's own.  The next rows'
+  // residual is on its way meanwhile.
+  template <int M, Res RES, int OUT, class W>
+  QMOE_D void way(int row0, W&& write) const {
+    const bool wide = N % Piece<OUT>::E == 0;
+    Residual<RES, OUT> res[2];
+    if (wide) load<RES, OUT>(row0, res[0]);
+    static_for<M>([&](auto m) {
+      write(m);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if constexpr (m + 1 < M)
+        if (wide) load<RES, OUT>(row0 + 32 * (m + 1), res[(m + 1) & 1]);
+      math();
+      if constexpr (OUT == QUANT) store_codes(row0 + 32 * m);
+      else if (wide) store_rows<RES, OUT>(row0 + 32 * m, res[m & 1]);
+      else store_each<RES, OUT>(row0 + 32 * m);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    });
+  }
+  template <int M, int OUT, class W>
+  QMOE_D void ways(int row0, W&& write) const {
+    if (GLU || !e.res) {
+      way<M, kNone, OUT>(row0, write);
+    } else if constexpr (!GLU) {
+      if (e.res_bf) way<M, kBF16, OUT>(row0, write);
+      else way<M, kF32, OUT>(row0, write);
     }
   }
-
-  QMOE_D void store(size_t at, const float (&v)[8]) const {
-    if (GLU && e.out > kOutBF16) {  // N % 32 == 0: a block's four lanes are all here
-      store_act8<QUANT>(v, at, e.y, e.scales);
-    } else if (!wide) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c0 + k < N) store_at(e, at + k, v[k]);
-    } else if (e.out == kOutF32) {
-      float* const y = (float*)e.y + at;
-      *(float4*)y = make_float4(v[0], v[1], v[2], v[3]);
-      if (c0 + 4 < N) *(float4*)(y + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint16_t* const y = (uint16_t*)e.y + at;
-      const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                 pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-      if (wide8) {
-        *(uint4*)y = w;
-      } else {
-        *(uint2*)y = make_uint2(w.x, w.y);
-        if (c0 + 4 < N) *(uint2*)(y + 4) = make_uint2(w.z, w.w);
-      }
-    }
+  template <int M, class W>
+  QMOE_D void all(int row0, W&& write) const {
+    if constexpr (GLU)
+      if (e.out > kOutBF16) return way<M, kNone, QUANT>(row0, write);
+    if (e.out == kOutBF16) ways<M, kOutBF16>(row0, write);
+    else ways<M, kOutF32>(row0, write);
   }
 };
 

@@ -44,6 +44,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "copy.hpp"
 #include "epilogue.hpp"
 
 #pragma clang fp contract(off)
@@ -130,29 +131,6 @@ QMOE_D v16f_t mx_mma32(const ActOp<XF8>& x, uint32_t sa, uint4 b, uint32_t sb, v
                                                            (int)sb);
   }
 }
-
-// a block-uniform address in scalar registers
-QMOE_D const uint8_t* uniform(const uint8_t* p) {
-  const uint64_t a = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-  return (const uint8_t*)((uint64_t)hi << 32 | lo);
-}
-
-// 16 bytes a lane from base + off to LDS address lds + 16 * lane.  It has no
-// output register; its completion is counted with the vector loads, in order,
-// and waited for by wait_copies before the barrier that hands the data over.
-// The compiler does not count it: its own waits for vector loads can only be
-// longer than needed.  m0 is declared as written, so that no value of the
-// compiler's own is taken to survive there (its warning that m0 is one of its
-// reserved registers is expected).
-QMOE_D void copy_to_lds(uint32_t lds, const uint8_t* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(base)
-               : "m0", "memory");
-}
-QMOE_D void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // FINE: MXFP8 products without the op's loss, at twice the ops; for results in fp32.
 // (Rounded to bf16 or to codes, a result has an error a thousand times that loss.)
@@ -438,16 +416,13 @@ __global__ __launch_bounds__(T::THREADS) void mx_tile_kernel(MxProduct P, int ti
   float* const out = (float*)smem + wave * 32 * T::PITCH;
   const Leave<T::COLS, GLU, XF8 ? kOutMx8 : kOutMx4> leave(
       P.e, out, n0 + (GLU ? wn / 2 : wn), P.R, P.N, lane);
-  static_for<TM>([&](auto mm) {
-    constexpr int m = decltype(mm)::value;
-    const int row0 = r0 + wm + 32 * m;
-    const auto res = leave.residual(row0);
+  leave.template all<TM>(r0 + wm, [&](auto m) {
 #pragma unroll
     for (int n = 0; n < TN; ++n)
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        out[(8 * (j >> 2) + 4 * h + (j & 3)) * T::PITCH + 32 * n + i] = acc[m][n][j];
-    leave.rows(row0, res);
+        out[(8 * (j >> 2) + 4 * h + (j & 3)) * T::PITCH + 32 * n + i] =
+            acc[decltype(m)::value][n][j];
   });
 }
 

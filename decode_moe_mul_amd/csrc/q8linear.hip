@@ -5,13 +5,13 @@
 //   y = act(p + bias) + res,  or  v = act(p_gate + bias_gate) * (p_up + bias_up)
 //
 // A 32-value block's integer sum is exact; its scaling and the sum over blocks are
-// fp32.  That scaling is what bounds many rows: a conversion, a product of the two
-// scales and a multiply-add for every output and block, 48 cycles of a SIMD beside
-// the 16 that the matrix core takes for the block's 16 x 16 x 32 products.
+// fp32.  That scaling is what bounds many rows: an output and block takes a
+// conversion, the product of the two scales and a multiply-add.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
 
+#include "copy.hpp"
 #include "product.hpp"
 
 #pragma clang fp contract(off)
@@ -19,7 +19,9 @@
 namespace qmoe {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 struct Q8Product {
   const int8_t* wq;    // [N][K]; of the gate where there are two products
@@ -158,184 +160,228 @@ static int launch_rows(const Q8Product& P, hipStream_t s) {
 }
 
 // ------------------------------------------------------ many rows ------
-// A block computes BM = 16 WR MI activation rows x BN = 64 WC weight rows with WR x WC
-// waves of MI x 4 16x16 results.  K advances 64 values (two blocks) per step; a
-// step's operand tiles are loaded once per block, 16 bytes a lane, one step ahead in
-// registers, and written to one of two LDS buffers with 80-byte rows (64 + 16 of
-// padding: the 16 rows one operand read touches fall on distinct banks).  Scales lie
-// block-major behind them, so that the four rows of a result are one 16-byte read.
-// Rows past the ends repeat the last one and are never stored; a block past K's end
-// repeats the last one with scale 0.
+// A block computes BM = 32 WR TM activation rows x BN = 32 WC TN weight rows with
+// WR x WC waves of TM x TN 32x32x32 ops, one to a 32-value block.  The products of a
+// block's scales, dw[n] d[r] for 32 x 32 outputs, are a matrix product too, with one
+// term: a 32x32x2 op in fp32 gives them rounded once, in the registers of the integer
+// sums.  That leaves the vector unit a conversion and a multiply-add an output and
+// block, 128 cycles of a SIMD beside the matrix core's 96 (three vector operations,
+// 192 cycles, and 16 x 16 ops took 700 x 2048 x 7168 pairs 153 us).
+//
+// K advances 128 values (four blocks) a step.  Codes go from memory to LDS without
+// passing registers, whole 128-byte lines, into one of two buffers, a step ahead;
+// scales pass through registers (their rows have any alignment) and lie as fp32, four to
+// a row.  The 16-byte chunk c of tile row q lies at chunk c ^ ((q >> 1) & 7), so that the
+// rows one operand read touches spread over the banks.  Rows past the ends repeat the
+// last one and are never stored; blocks past K's end repeat the row's last one with
+// scale 0.
 //
 // KS teams of WR x WC waves split K where there are too few tiles to fill the part,
 // as in the MX tiles; a gated pair's weight rows are 32 of the gate, 32 of up.
-template <int WR_, int WC_, int MI_, int KS_>
+template <int WR_, int WC_, int TM_, int TN_, int KS_>
 struct Q8Tile {
-  static constexpr int WR = WR_, WC = WC_, MI = MI_, KS = KS_, NB = 4;
-  static constexpr int BM = 16 * WR * MI, BN = 64 * WC, ROWS = BM + BN, NW = WR * WC;
+  static constexpr int WR = WR_, WC = WC_, TM = TM_, TN = TN_, KS = KS_;
+  static constexpr int BM = 32 * WR * TM, BN = 32 * WC * TN, ROWS = BM + BN, NW = WR * WC;
   static constexpr int TEAM = 64 * NW, THREADS = TEAM * KS;
-  static constexpr int ROW = 80, BUF = ROWS * (ROW + 8);  // bytes: codes, then two scales a row
-  static constexpr int CH = ROWS * 4 / TEAM;              // 16-byte chunks per thread and step
-  static constexpr int SC = (ROWS + TEAM - 1) / TEAM;     // rows whose scales a thread loads
-  static_assert(MI % 2 == 0 && ROWS * 4 % TEAM == 0 && BM * 4 % TEAM == 0, "");
-  static constexpr int PITCH = leave_pitch(64), OUT = NW * 32 * PITCH * 4;
-  static constexpr int SUMS = MI * NB * 4 * TEAM * 4;
+  static constexpr int CODES = ROWS * 128, BUF = CODES + ROWS * 16;  // bytes
+  static constexpr int JA = BM / 8 / NW, J = ROWS / 8 / NW;          // copies per wave and step
+  static constexpr int SC = (ROWS + TEAM - 1) / TEAM;  // rows whose scales a thread loads
+  static_assert(NW % 2 == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TN % 2 == 0, "");
+  static constexpr int COLS = 32 * TN, PITCH = leave_pitch(COLS), OUT = NW * 32 * PITCH * 4;
+  static constexpr int SUMS = TM * TN * 16 * TEAM * 4;
   static constexpr size_t LDS = std::max(KS * 2 * BUF, OUT + (KS - 1) * SUMS);
   static_assert(LDS <= 160 << 10, "");
 };
 
+// (Two waves to a SIMD leave a wave 256 registers, all of which the vector unit reads;
+// with 512 the compiler puts the ops' results where it does not and copies each.)
 template <class T, bool GLU>
-__global__ __launch_bounds__(T::THREADS) void q8_tile_kernel(Q8Product P, int tiles_m) {
-  constexpr int MI = T::MI, NB = T::NB;
+__global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_kernel(Q8Product P, int tiles_m,
+                                                             int tiles_n) {
+  constexpr int TM = T::TM, TN = T::TN, M = TM * TN;
   extern __shared__ __align__(16) uint8_t smem[];
   const int team = T::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / T::TEAM);
-  const int tid = threadIdx.x % T::TEAM, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x % T::TEAM, lane = tid & 63, i = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r0 = (int)(blockIdx.x % tiles_m) * T::BM;
-  const int n0 = (int)(blockIdx.x / tiles_m) * (GLU ? T::BN / 2 : T::BN);
-  const int nb = P.K >> 5, all = (nb + 1) >> 1;
+  // a run of tiles to each XCD, down the rows first, as in the MX tiles
+  const int T_ = tiles_m * tiles_n, per = T_ >> 3, extra = T_ & 7;
+  const int xcd = blockIdx.x & 7;
+  const int tile = xcd * per + min(xcd, extra) + (blockIdx.x >> 3);
+  const int r0 = (tile % tiles_m) * T::BM, n0 = (tile / tiles_m) * (GLU ? T::BN / 2 : T::BN);
+  const int nb = P.K >> 5, all = (nb + 3) >> 2;
   const int loops = (all + T::KS - 1) / T::KS;  // steps of a team, the last one's fewer
   const int first = team * loops, steps = min(max(all - first, 0), loops);
   uint8_t* const mem = smem + team * 2 * T::BUF;
-  const auto codes = [&](int buf) { return mem + buf * T::BUF; };
-  const auto scales = [&](int buf) { return (float*)(mem + buf * T::BUF + T::ROWS * T::ROW); };
+  const int8_t* const abase = P.xq + (size_t)r0 * P.K;
+  const int8_t* const bbase = P.wq + (size_t)n0 * P.K;
+  const int8_t* const bbase2 = GLU ? P.wq2 + (size_t)n0 * P.K : nullptr;
+  const int arows = P.R - r0 - 1, brows = P.N - n0 - 1;  // last valid row of the tile
   const auto weight = [](int q) { return GLU ? (q >> 6 << 5) + (q & 31) : q; };
-  const auto is_up = [](int q) { return GLU && (q >> 5 & 1); };
 
-  // chunk c = tid + j TEAM: row c >> 2 of the tile (activations first), bytes 16 (c & 3)
-  const int8_t* src[T::CH];
+  // Copy j of the wave fills 8 rows of the tile.
+  const int rem = nb - 4 * (all - 1);  // blocks of K's last step, 1..4
+  const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);  // NW is even: for every j
+  const uint32_t over = 32u * (uint32_t)max((chunk >> 1) - (rem - 1), 0);
+  uint32_t off[T::J];
 #pragma unroll
-  for (int j = 0; j < T::CH; ++j) {
-    const int q = (tid + j * T::TEAM) >> 2, qb = q - T::BM;
-    src[j] = q < T::BM ? P.xq + (size_t)min(r0 + q, P.R - 1) * P.K
-                       : (is_up(qb) ? P.wq2 : P.wq) + (size_t)min(n0 + weight(qb), P.N - 1) * P.K;
+  for (int j = 0; j < T::J; ++j) {
+    const int q = 8 * (wave + T::NW * (j < T::JA ? j : j - T::JA)) + (lane >> 3);
+    const int row = j < T::JA ? min(q, arows) : min(weight(q), brows);
+    off[j] = (uint32_t)row * (uint32_t)P.K + 16u * (uint32_t)chunk;
   }
-  i32x4_t cr[T::CH];
-  float sr[T::SC][2];
-  const auto load = [&](int st) {
-    const int b0 = 2 * min(first + st, all - 1), b1 = min(b0 + 1, nb - 1);
-    const bool second = b0 + 1 < nb;
-    const int ch = 16 * (tid & 3);  // TEAM is a multiple of 4
-    const int k0 = ch < 32 ? b0 * 32 + ch : b1 * 32 + ch - 32;
-    static_for<T::CH>([&](auto j) { cr[j] = *(const i32x4_t*)(src[j] + k0); });
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)mem;
+  const auto copy = [&](int st, int j) {
+    const int k = min(first + st, all - 1);  // past the team's steps: unused
+    const int8_t* base = j < T::JA ? abase : bbase;
+    if (GLU && j >= T::JA && ((wave + T::NW * (j - T::JA)) >> 2 & 1)) base = bbase2;
+    copy_to_lds(lds0 + (st & 1) * T::BUF + (wave + T::NW * j) * 1024,
+                uniform((const uint8_t*)base + (size_t)k * 128), off[j] - (k + 1 == all ? over : 0));
+  };
+  f32x4_t sreg[T::SC];
+  const auto load_scales = [&](int st) {
+    const int b0 = 4 * min(first + st, all - 1);
+    const bool whole = b0 + 4 <= nb;
     static_for<T::SC>([&](auto j) {
       const int q = min(tid + j * T::TEAM, T::ROWS - 1), qb = q - T::BM;
+      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
       if (q < T::BM) {
-        const float* d = P.xd + (size_t)min(r0 + q, P.R - 1) * nb;
-        sr[j][0] = d[b0];
-        sr[j][1] = second ? d[b1] : 0.f;
+        const float* d = P.xd + (size_t)(r0 + min(q, arows)) * nb + b0;
+        if (whole) __builtin_memcpy(&v, d, 16);
+        else
+          for (int b = 0; b < nb - b0; ++b) v[b] = d[b];
       } else {
-        const uint16_t* d =
-            (is_up(qb) ? P.wd2 : P.wd) + (size_t)min(n0 + weight(qb), P.N - 1) * nb;
-        sr[j][0] = f16_bits_to_f32(d[b0]);
-        sr[j][1] = second ? f16_bits_to_f32(d[b1]) : 0.f;
+        const uint16_t* d = (GLU && (qb >> 5 & 1) ? P.wd2 : P.wd) +
+                            (size_t)(n0 + min(weight(qb), brows)) * nb + b0;
+        if (whole) {
+          uint32_t w[2];
+          __builtin_memcpy(w, d, 8);
+          v = f32x4_t{f16_bits_to_f32(w[0] & 0xFFFFu), f16_bits_to_f32(w[0] >> 16),
+                      f16_bits_to_f32(w[1] & 0xFFFFu), f16_bits_to_f32(w[1] >> 16)};
+        } else {
+          for (int b = 0; b < nb - b0; ++b) v[b] = f16_bits_to_f32(d[b]);
+        }
       }
+      sreg[j] = v;
     });
   };
-  const auto write = [&](int buf) {
-    static_for<T::CH>([&](auto j) {
-      const int c = tid + j * T::TEAM;
-      *(i32x4_t*)(codes(buf) + (c >> 2) * T::ROW + 16 * (c & 3)) = cr[j];
-    });
+  const auto store_scales = [&](int st) {
     static_for<T::SC>([&](auto j) {
       const int q = tid + j * T::TEAM;
-      if (T::ROWS % T::TEAM == 0 || q < T::ROWS) {
-        scales(buf)[q] = sr[j][0];
-        scales(buf)[T::ROWS + q] = sr[j][1];
-      }
+      if (T::ROWS % T::TEAM == 0 || q < T::ROWS)
+        *(f32x4_t*)(mem + (st & 1) * T::BUF + T::CODES + q * 16) = sreg[j];
     });
   };
-  const int wm = (wave / T::WC) * 16 * MI, wn = (wave % T::WC) * 64;
-  f32x4_t acc[MI][NB];
+  const int wm = (wave / T::WC) * 32 * TM, wn = (wave % T::WC) * 32 * TN;
+  const auto row_of = [&](int r) { return r < TM ? wm + 32 * r + i : T::BM + wn + 32 * (r - TM) + i; };
+  f32x16_t acc[TM][TN];
 #pragma unroll
-  for (int m = 0; m < MI; ++m)
+  for (int m = 0; m < TM; ++m)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[m][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const auto compute = [&](int buf) {
-    // one block at a time: unrolling both keeps twice the operands live
-#pragma unroll 1
-    for (int kb = 0; kb < 2; ++kb) {
-      // lane (li, g) supplies codes 8 g .. + 7 of the block of its row; the result
-      // holds activation rows 4 g + j, weight row li
-      long bq[NB], aq[MI];
-      float bs[NB];
+    for (int n = 0; n < TN; ++n)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int q = T::BM + wn + 16 * b + li;
-        bq[b] = *(const long*)(codes(buf) + q * T::ROW + 32 * kb + 8 * g);
-        bs[b] = scales(buf)[kb * T::ROWS + q];
-      }
+      for (int j = 0; j < 16; ++j) acc[m][n][j] = 0.f;
+  // A step's 4 M pairs of ops in turn: the next pair is issued before the vector unit
+  // takes the last one's results, and a block's operands are read a block ahead.
+  i32x16_t bias;  // 1.5 2^23 as fp32: a sum below 2^22 added to its bits is added to it
 #pragma unroll
-      for (int m = 0; m < MI; ++m)
-        aq[m] = *(const long*)(codes(buf) + (wm + 16 * m + li) * T::ROW + 32 * kb + 8 * g);
-      i32x4_t is[MI][NB];
+  for (int j = 0; j < 16; ++j) bias[j] = 0x4B400000;
+  const auto compute = [&](int st) {
+    const uint8_t* const buf = mem + (st & 1) * T::BUF;
+    f32x4_t sc[TM + TN];
+    i32x4_t q[2][TM + TN];
+    f32x16_t sum[2], mul[2];
+    const auto read = [&](auto b) {
+      static_for<TM + TN>([&](auto r) {
+        q[b & 1][r] = *(const i32x4_t*)(buf + row_of(r) * 128 + 16 * ((2 * b + h) ^ ((i >> 1) & 7)));
+      });
+    };
+    const auto sums = [&](auto t) {
+      constexpr int b = t / M, m = t % M / TN, n = t % TN;
+      sum[t & 1] = __builtin_bit_cast(f32x16_t, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                       q[b & 1][m], q[b & 1][TM + n], bias, 0, 0, 0));
+    };
+    const auto muls = [&](auto t) {
+      constexpr int b = t / M, m = t % M / TN, n = t % TN;
+      f32x16_t zero;
 #pragma unroll
-      for (int m = 0; m < MI; ++m)
+      for (int j = 0; j < 16; ++j) zero[j] = 0.f;
+      mul[t & 1] = __builtin_amdgcn_mfma_f32_32x32x2f32(sc[m][b], sc[TM + n][b], zero, 0, 0, 0);
+    };
+    read(Int<0>{});
+    static_for<TM + TN>([&](auto r) {
+      sc[r] = *(const f32x4_t*)(buf + T::CODES + row_of(r) * 16);
+      // the op's second term is none: the upper lanes' activation scales are zero
+      if constexpr (r < TM)
+        if (h) sc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    });
+    sums(Int<0>{});
+    muls(Int<0>{});
+    static_for<4 * M>([&](auto t) {
+      constexpr int b = t / M, m = t % M / TN, n = t % TN;
+      if constexpr (t % M == 0 && b < 3) read(Int<b + 1>{});
+      if constexpr (t + 1 < 4 * M) sums(Int<t + 1>{});
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          is[m][b] = __builtin_amdgcn_mfma_i32_16x16x32_i8(aq[m], bq[b], i32x4_t{0, 0, 0, 0}, 0,
-                                                          0, 0);
+      for (int j = 0; j < 16; ++j) sum[t & 1][j] -= 12582912.f;
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (t + 1 < 4 * M) muls(Int<t + 1>{});
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < MI; ++m) {
-        const float4 a4 = *(const float4*)(scales(buf) + kb * T::ROWS + wm + 16 * m + 4 * g);
-        const float as[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[m][b][j] = fmaf((float)is[m][b][j], as[j] * bs[b], acc[m][b][j]);
-      }
-    }
+      for (int j = 0; j < 16; ++j)
+        acc[m][n][j] = fmaf(sum[t & 1][j], mul[t & 1][j], acc[m][n][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
-  // buffer st & 1 holds step st; the next one is on its way in registers.  Loads past
-  // the team's steps repeat the last one: their buffer is not used.
-  load(0);
-  write(0);
+  // Buffer st & 1 holds step st; the next step's codes are on their way to the other,
+  // the scales of the one after it in registers.  What is fetched past a team's steps
+  // repeats the last one and is not used.
+  static_for<T::J>([&](auto j) { copy(0, j); });
+  load_scales(0);
+  store_scales(0);
+  load_scales(1);
+  wait_copies();
   __syncthreads();
-  load(1);
+#pragma unroll 1
   for (int st = 0; st < loops; ++st) {
-    if (st < steps) compute(st & 1);
-    write((st + 1) & 1);
+    static_for<T::J>([&](auto j) { copy(st + 1, j); });
+    store_scales(st + 1);
+    load_scales(st + 2);
+    if (st < steps) compute(st);
+    wait_copies();
     __syncthreads();
-    load(st + 2);
   }
   if constexpr (T::KS > 1) {
     float* const sums = (float*)(smem + T::OUT) + tid;
 #pragma unroll
-    for (int m = 0; m < MI; ++m)
+    for (int m = 0; m < TM; ++m)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int n = 0; n < TN; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (team > 0)
-            sums[((team - 1) * MI * NB * 4 + (m * NB + b) * 4 + j) * T::TEAM] = acc[m][b][j];
+        for (int j = 0; j < 16; ++j)
+          if (team > 0) sums[((team - 1) * M * 16 + (m * TN + n) * 16 + j) * T::TEAM] = acc[m][n][j];
     __syncthreads();
     if (team > 0) return;
 #pragma unroll 1
     for (int t = 0; t < T::KS - 1; ++t)
 #pragma unroll
-      for (int m = 0; m < MI; ++m)
+      for (int m = 0; m < TM; ++m)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int n = 0; n < TN; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[m][b][j] += sums[(t * MI * NB * 4 + (m * NB + b) * 4 + j) * T::TEAM];
+          for (int j = 0; j < 16; ++j)
+            acc[m][n][j] += sums[(t * M * 16 + (m * TN + n) * 16 + j) * T::TEAM];
   }
+  // Register 4 a + b of a 32 x 32 block is row 8 a + 4 h + b, column i.
   float* const out = (float*)smem + wave * 32 * T::PITCH;
-  const Leave<64, GLU, kOutQ8> leave(P.e, out, n0 + (GLU ? wn / 2 : wn), P.R, P.N, lane);
+  const Leave<T::COLS, GLU, kOutQ8> leave(P.e, out, n0 + (GLU ? wn / 2 : wn), P.R, P.N, lane);
+  leave.template all<TM>(r0 + wm, [&](auto m) {
 #pragma unroll
-  for (int m = 0; m < MI; m += 2) {
-    const int row0 = r0 + wm + 16 * m;
-    const auto res = leave.residual(row0);
+    for (int n = 0; n < TN; ++n)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          out[(16 * t + 4 * g + j) * T::PITCH + 16 * b + li] = acc[m + t][b][j];
-    leave.rows(row0, res);
-  }
+      for (int j = 0; j < 16; ++j)
+        out[(8 * (j >> 2) + 4 * h + (j & 3)) * T::PITCH + 32 * n + i] =
+            acc[decltype(m)::value][n][j];
+  });
 }
 
 template <class T, bool GLU>
@@ -353,17 +399,17 @@ static int launch_q8(const Q8Product& P, hipStream_t s) {
     declared.fetch_or(bit, std::memory_order_relaxed);
   }
   return QMOE_LAUNCH("q8_tile", (q8_tile_kernel<T, GLU>), dim3((unsigned)(tm * tn)), T::THREADS,
-                     T::LDS, s, P, tm);
+                     T::LDS, s, P, tm, tn);
 }
 
 struct Q8Choice {
   int bm, cols, threads, slots;
-  float us;
+  float us, alone;
   int (*launch)(const Q8Product&, hipStream_t);
 };
 template <class T, bool GLU>
-static constexpr Q8Choice q8_choice(int slots, float us) {
-  return {T::BM, GLU ? T::BN / 2 : T::BN, T::THREADS, slots, us, launch_q8<T, GLU>};
+static constexpr Q8Choice q8_choice(int slots, float us, float alone) {
+  return {T::BM, GLU ? T::BN / 2 : T::BN, T::THREADS, slots, us, alone, launch_q8<T, GLU>};
 }
 
 template <bool GLU>
@@ -381,18 +427,19 @@ static int run(const ProductCall& c, hipStream_t s) {
       if (P.e.out == kOutQ8) return launch_rows<true, 2>(P, s);
     return launch_rows<GLU, 1>(P, s);
   }
-  // rounds of tiles times the time of one, as for the MX tiles
-  static constexpr Q8Choice choices[] = {q8_choice<Q8Tile<1, 2, 2, 4>, GLU>(1, 30.f),
-                                         q8_choice<Q8Tile<2, 2, 2, 2>, GLU>(1, 45.f),
-                                         q8_choice<Q8Tile<2, 2, 4, 1>, GLU>(2, 130.f)};
+  static constexpr Q8Choice choices[] = {q8_choice<Q8Tile<1, 2, 1, 2, 3>, GLU>(1, 30.f, 30.f),
+                                         q8_choice<Q8Tile<2, 2, 1, 2, 2>, GLU>(1, 37.f, 37.f),
+                                         q8_choice<Q8Tile<2, 2, 1, 2, 1>, GLU>(2, 65.f, 50.f),
+                                         q8_choice<Q8Tile<2, 2, 2, 2, 1>, GLU>(2, 109.f, 75.f)};
   const int cus = std::max(1, cu_count());
   const Q8Choice* best = nullptr;
   float least = 0.f;
   for (const Q8Choice& q : choices) {
     const long long tiles = (long long)((P.R + q.bm - 1) / q.bm) * ((P.N + q.cols - 1) / q.cols);
     if (tiles > 0xFFFFFFFFLL / q.threads) continue;
-    const long long at_once = (long long)q.slots * cus;
-    const float us = q.us * (float)((tiles + at_once - 1) / at_once);
+    const long long at_once = (long long)q.slots * cus, last = tiles % at_once;
+    const float us = q.us * (float)(tiles / at_once) +
+                     (last == 0 ? 0.f : last <= cus ? q.alone : q.us);
     if (!best || us < least) best = &q, least = us;
   }
   if (!best) return fail(QMOE_ERR_UNSUPPORTED, "%s: R=%d N=%d: too many tiles", c.who, c.R, c.N);
