@@ -15,6 +15,14 @@ namespace qmoe {
 template <int WR, int WC, int TM, int TN, int KS>
 using T4 = Tile<WR, WC, TM, TN, KS, false>;
 
+// Which kernel: as measured at K = 4096 (us; N counts the pair's columns).
+//   rows  1 x 14336: 13.7, 16 x 14336: 16.3; 32 x 64: 14.3; 64 x 64: 13.7 (62 MB of
+//     weights; a streaming read of as many takes 12)
+//   32 x 64, three teams  40 x 4096: 8.1; 64 x 64: 8.5; 128 x 64: 11.1
+//   64 x 64, two teams    128 x 4096: 9.0; 32 x 64: 9.1; 128 x 64: 11.4
+//   128 x 64, two teams   700 x 2048 (K = 7168): 20.4; 64 x 64: 31; two to a unit: 23.5
+//   128 x 64, two to a unit  2048 x 14336: 147; two teams: 202; 256 x 128: 149-158
+// The largest tile is chosen where it saves a round.
 static int run(const ProductCall& c, hipStream_t s) {
   const int st = check_product(c);
   if (st) return st == kNothing ? QMOE_OK : st;
@@ -24,9 +32,9 @@ static int run(const ProductCall& c, hipStream_t s) {
     return P.e.out > kOutBF16 ? launch_rows<false, true, 2>("mxfp4_glu_rows", P, s)
                               : launch_rows<false, true, 1>("mxfp4_glu_rows", P, s);
   static constexpr Choice choices[] = {
-      choice<T4<1, 2, 1, 2, 2>, true>(1, 10.f), choice<T4<2, 2, 1, 2, 2>, true>(1, 11.f),
-      choice<T4<2, 2, 2, 2, 2>, true>(1, 15.f), choice<T4<2, 2, 2, 2, 1>, true>(2, 25.f),
-      choice<T4<2, 2, 4, 4, 1>, true>(1, 33.f)};
+      choice<T4<1, 2, 1, 2, 3>, true>(1, 9.2f), choice<T4<2, 2, 1, 2, 2>, true>(1, 9.5f),
+      choice<T4<2, 2, 2, 2, 2>, true>(1, 12.5f), choice<T4<2, 2, 2, 2, 1>, true>(2, 21.f, 14.f),
+      choice<T4<2, 2, 4, 4, 1>, true>(1, 36.f)};
   return launch_choice(choices, c.who, "mxfp4_glu_tile", P, s);
 }
 

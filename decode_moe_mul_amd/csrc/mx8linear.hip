@@ -15,15 +15,24 @@ namespace qmoe {
 template <int WR, int WC, int TM, int TN, int KS>
 using T8 = Tile<WR, WC, TM, TN, KS, true>;
 
+// Which kernel: as measured at K = 4096 with bf16 results (us).
+//   rows  1 x 4096: 3.8
+//   32 x 64, four teams    128 x 4096: 6.4; 64 x 64: 7.9; 64 x 128: 9.2
+//   64 x 64, three teams   333 x 2050 (K = 7200): 17.2; 32 x 64: 22.9; 64 x 128: 21.4
+//   64 x 128, two teams    2048 x 4096: 58.7
+//   128 x 128              2048 x 4096: 41.8;  (K = 14336) 121
+//   128 x 256              2048 x 4096: 38.9;  (K = 14336) 112; 2048 x 14336 with fp32
+//     results 243, 128 x 128: 213
+// (An activation row has 256 bytes a step: LDS holds no two of the larger tiles.)
 template <bool FINE>
 static int launch(const ProductCall& c, const MxProduct& P, hipStream_t s) {
   const int cus = std::max(1, cu_count());
   if (P.R <= 16 && P.N <= 32 * cus) return launch_rows<true, false, 1, FINE>("mxfp8_rows", P, s);
-  static constexpr Choice choices[] = {choice<T8<1, 2, 1, 1, 4>, false, FINE>(1, 8.f),
-                                       choice<T8<2, 2, 1, 1, 3>, false, FINE>(1, 11.f),
+  static constexpr Choice choices[] = {choice<T8<1, 2, 1, 1, 4>, false, FINE>(1, 6.6f),
+                                       choice<T8<2, 2, 1, 1, 3>, false, FINE>(1, 9.5f),
                                        choice<T8<2, 2, 1, 2, 2>, false, FINE>(1, 14.f),
-                                       choice<T8<2, 2, 2, 2, 1>, false, FINE>(1, 22.f),
-                                       choice<T8<2, 2, 2, 4, 1>, false, FINE>(1, 40.f)};
+                                       choice<T8<2, 2, 2, 2, 1>, false, FINE>(1, FINE ? 30.f : 20.5f),
+                                       choice<T8<2, 2, 2, 4, 1>, false, FINE>(1, FINE ? 61.f : 38.f)};
   return launch_choice(choices, c.who, "mxfp8_tile", P, s);
 }
 

@@ -446,17 +446,19 @@ static int launch_tile(const char* name, const MxProduct& P, hipStream_t s) {
 
 struct Choice {
   int bm, cols, threads, slots;
-  float us;
+  float us, alone;
   int (*launch)(const char*, const MxProduct&, hipStream_t);
 };
 template <class T, bool GLU, bool FINE = false>
-static constexpr Choice choice(int slots, float us) {
-  return {T::BM, GLU ? T::BN / 2 : T::BN, T::THREADS, slots, us, launch_tile<T, GLU, FINE>};
+static constexpr Choice choice(int slots, float us, float alone = 0.f) {
+  return {T::BM, GLU ? T::BN / 2 : T::BN, T::THREADS, slots, us, alone > 0.f ? alone : us,
+          launch_tile<T, GLU, FINE>};
 }
 
 // A round of tiles takes about as long as one tile, so with K given the choice
-// goes by rounds times the time of one, with `slots` tiles to a compute unit.  A
-// launch has fewer than 2^32 threads: a tile that would need more is passed over.
+// goes by rounds times the time of one, with `slots` tiles to a compute unit (`alone`:
+// where a last round leaves each unit one of them).  A launch has fewer than 2^32
+// threads: a tile that would need more is passed over.
 template <int C>
 static int launch_choice(const Choice (&choices)[C], const char* who, const char* name,
                          const MxProduct& P, hipStream_t s) {
@@ -467,8 +469,9 @@ static int launch_choice(const Choice (&choices)[C], const char* who, const char
     const long long tiles =
         (long long)((P.R + c.bm - 1) / c.bm) * ((P.N + c.cols - 1) / c.cols);
     if (tiles > 0xFFFFFFFFLL / c.threads) continue;
-    const long long at_once = (long long)c.slots * cus;
-    const float us = c.us * (float)((tiles + at_once - 1) / at_once);
+    const long long at_once = (long long)c.slots * cus, last = tiles % at_once;
+    const float us = c.us * (float)(tiles / at_once) +
+                     (last == 0 ? 0.f : last <= cus ? c.alone : c.us);
     if (!best || us < least) {
       best = &c;
       least = us;

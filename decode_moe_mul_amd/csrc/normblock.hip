@@ -252,7 +252,16 @@ static int run_norm_block(const char* who, const NormBlockCall& c) {
       !QMOE_ALIGNED(c.out, 16) || (OUT == kOutQ8 && !QMOE_ALIGNED(c.scales, 4)))
     return fail(QMOE_ERR_INVALID_ARG, "%s: misaligned pointer", who);
   const int K8 = c.K >> 3, cus = std::max(1, cu_count());
-  int npt = K8 <= 512 ? 1 : c.R <= 2 * cus ? 2 : 4, tpr = 4;
+  const bool xbf = c.x_dtype == QMOE_BF16, rbf = c.res_dtype == QMOE_BF16;
+  // Octets per thread.  Few rows: one up to 4096 values (1 x 4096 4.7 us, with two 5.3,
+  // with four 8.1), two beyond (16 x 7168 6.2; one 6.9, four 7.3).  Once the rows fill
+  // the part, fewer barriers and sums per byte pay, as far as the registers go: four of
+  // bf16 (8192 x 7168 124 us; two 142, one 196; 8192 x 4096 61; two 68, one 79; eight
+  // 140), two where fp32 is among them (8192 x 7168 166; four 185, one 215) and for rows
+  // below 2048 values (8192 x 256 6.6; four 7.3, one 6.8).  Two rows of two octets to a
+  // thread, which share the weights and the barriers, take 147 at 8192 x 7168.
+  const bool many = c.R > 2 * cus;
+  int npt = many ? (xbf && rbf && K8 >= 256 ? 4 : 2) : K8 <= 512 ? 1 : 2, tpr = 4;
   while (tpr < 1024 && tpr * npt < K8) tpr *= 2;
   while (tpr * npt < K8) npt *= 2;  // longer rows than 1024 threads hold: more per thread
   const int block = std::max(tpr, 256), rows = block / tpr;
@@ -262,7 +271,6 @@ static int run_norm_block(const char* who, const NormBlockCall& c) {
                           c.w,   c.out,    c.scales,    c.eps_post, c.scale,
                           c.res_scale, c.eps, c.R, c.K, c.gate && c.gate_dtype == QMOE_BF16,
                           c.gate ? c.R / c.gate_rows : 1};
-  const bool xbf = c.x_dtype == QMOE_BF16, rbf = c.res_dtype == QMOE_BF16;
   hipStream_t s = (hipStream_t)c.stream;
   if (npt == 1) return launch_norm_block<OUT, 1>(xbf, rbf, grid, block, s, P, tpr);
   if (npt == 2) return launch_norm_block<OUT, 2>(xbf, rbf, grid, block, s, P, tpr);

@@ -702,12 +702,12 @@ def gemm_mxfp4_mxfp4(W, N, K, codes, scales, dtype=None, out=None):
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4, "relu2": 5}
 
 
-def _product_args(fmt, N, K, codes, scales, act, *weights):
-    """(R, GPU index, activation code) of a product's operands."""
-    kinds, code = _ACT_TYPES.get(fmt), ACTIVATIONS.get(act)
+def _product_refused(fmt, N, K, codes, scales, act):
+    """Raise for what is wrong with a product's operands."""
+    kinds = _ACT_TYPES.get(fmt)
     if kinds is None:
         raise QmoeError(f"activation format {fmt!r} is not one of {ACT_FORMATS}")
-    if code is None:
+    if act not in ACTIVATIONS:
         raise QmoeError(f"activation {act!r} is not one of {tuple(ACTIVATIONS)}")
     if K <= 0 or K % 32 or K > _MOST or not 0 <= N <= _MOST:
         raise QmoeError(f"W [{N}, {K}]: N is at least 0, K a multiple of 32, both below 2^31")
@@ -719,16 +719,31 @@ def _product_args(fmt, N, K, codes, scales, act, *weights):
         _refuse("scales", scales, (R, K // 32), st, index)
     if R > _MOST:
         raise QmoeError(f"activations [{R}, {K}]: sizes are below 2^31")
-    # two planes, each from a 256-byte boundary on: int8 codes and fp16 scales, or
-    # 4-bit codes and one byte a scale
-    a, b = (256, 4096) if fmt == "q8" else (512, 8192)
-    need = (-(-N * K // a) - (-N * K // b)) * 256
-    for W in weights:
-        if (W.dtype is not _th.uint8 or W.get_device() != index or not W.is_contiguous()
-                or W.numel() < need):
-            raise QmoeError(f"weights must be a packed {'Q8_0' if fmt == 'q8' else 'MXFP4'} "
-                            f"[{N}, {K}] tensor on the activations' GPU")
-    return R, index, code
+    raise QmoeError(f"weights must be packed {'Q8_0' if fmt == 'q8' else 'MXFP4'} [{N}, {K}] "
+                    "tensors on the activations' GPU")
+
+
+def _product_args(fmt, N, K, codes, scales, act, W, W2=None):
+    """(R, GPU index, activation code) of a product's operands."""
+    kinds, code = _ACT_TYPES.get(fmt), ACTIVATIONS.get(act)
+    index, shape = codes.get_device(), codes.shape
+    if kinds is not None and code is not None and index >= 0 and len(shape) == 2:
+        per, ct, st = kinds
+        R, u8 = shape[0], _th.uint8
+        # two planes, each from a 256-byte boundary on: int8 codes and fp16 scales, or
+        # 4-bit codes and one byte a scale
+        need = ((N * K + 255 >> 8) + (N * K + 4095 >> 12) if per == 1 and ct is not u8 else
+                (N * K + 511 >> 9) + (N * K + 8191 >> 13)) << 8
+        if (0 < K <= _MOST and K % 32 == 0 and 0 <= N <= _MOST and R <= _MOST
+                and shape[1] == K // per and codes.dtype is ct and codes.is_contiguous()
+                and scales.dtype is st and scales.shape == (R, K // 32)
+                and scales.get_device() == index and scales.is_contiguous()
+                and W.dtype is u8 and W.get_device() == index and W.is_contiguous()
+                and W.numel() >= need
+                and (W2 is None or W2.dtype is u8 and W2.get_device() == index
+                     and W2.is_contiguous() and W2.numel() >= need)):
+            return R, index, code
+    _product_refused(fmt, N, K, codes, scales, act)
 
 
 def _bias(b, N, index, what):
