@@ -5,8 +5,8 @@
 //   y = act(p + bias) + res,  or  v = act(p_gate + bias_gate) * (p_up + bias_up)
 //
 // A 32-value block's integer sum is exact; its scaling and the sum over blocks are
-// fp32.  That scaling is what bounds many rows: an output and block takes a
-// conversion, the product of the two scales and a multiply-add.
+// fp32.  That scaling is what bounds many rows: an output and block takes the sum made
+// fp32, the product of the two scales and a multiply-add.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -164,9 +164,13 @@ static int launch_rows(const Q8Product& P, hipStream_t s) {
 // WR x WC waves of TM x TN 32x32x32 ops, one to a 32-value block.  The products of a
 // block's scales, dw[n] d[r] for 32 x 32 outputs, are a matrix product too, with one
 // term: a 32x32x2 op in fp32 gives them rounded once, in the registers of the integer
-// sums.  That leaves the vector unit a conversion and a multiply-add an output and
-// block, 128 cycles of a SIMD beside the matrix core's 96 (three vector operations,
-// 192 cycles, and 16 x 16 ops took 700 x 2048 x 7168 pairs 153 us).
+// sums.  Those start from the bits of 1.5 2^23, so that a subtraction makes them fp32.
+// That leaves the vector unit two operations an output and block.  700 x 2048 x 7168
+// pairs take 110 us: with 16 x 16 ops and three vector operations 153, with these ops
+// one after the other 112-147.  The fp32 op takes 64 cycles of the vector unit's own (a
+// probe: it and 16 multiply-adds take the sum of both, the integer op hides behind
+// them), about 211 a pair of ops in all; the scales as a bf16 op of their parts, which
+// does overlap, gained 2 %, because waits for copies and barriers are 38 % of a wave.
 //
 // K advances 128 values (four blocks) a step.  Codes go from memory to LDS without
 // passing registers, whole 128-byte lines, into one of two buffers, a step ahead;
@@ -310,9 +314,9 @@ __global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_
     read(Int<0>{});
     static_for<TM + TN>([&](auto r) {
       sc[r] = *(const f32x4_t*)(buf + T::CODES + row_of(r) * 16);
-      // the op's second term is none: the upper lanes' activation scales are zero
-      if constexpr (r < TM)
-        if (h) sc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      // the op's second term is none: the upper lanes' scales are zero, on both sides,
+      // since zero times a scale that is infinite would be NaN
+      if (h) sc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     });
     sums(Int<0>{});
     muls(Int<0>{});
@@ -422,6 +426,12 @@ static int run(const ProductCall& c, hipStream_t s) {
                     (const int8_t*)w2 + L.off[0], (const uint16_t*)(w2 + L.off[1]),
                     (const int8_t*)c.codes, (const float*)c.scales, c.N, c.K, c.R,
                     epilogue_of(c)};
+  // Which kernel: as measured (us; tiles at K = 4096).
+  //   rows  16 x 4096 (K = 14336): 20.6
+  //   32 x 128, three teams  a round of tiles: 30
+  //   64 x 128, two teams    37
+  //   64 x 128               two to a unit 65, one 50
+  //   128 x 128              two to a unit 109, one 75
   if (P.R <= 16) {
     if constexpr (GLU)
       if (P.e.out == kOutQ8) return launch_rows<true, 2>(P, s);

@@ -510,8 +510,8 @@ int qgemm_mxfp4_mxfp4(const void *W, int N, int K, const uint8_t *codes,
  *     h = res_scale * res + scale * gate * z         (rounded to fp32, then to
  *                                                     res_dtype; to res_out)
  *     y = h * w / sqrt(mean_k h^2 + eps), rounded to fp32, then to y_dtype
- *   Each line before its rounding is taken in fp64: h is the correctly rounded
- *   value, and y's fp32 value as well, but for values that near a rounding border.
+ *   Each line before its rounding is taken in fp64: h and y's fp32 value are the
+ *   correctly rounded ones, but for values within 2^-47 of a rounding border.
  *   x [R, K] (x_dtype) is the block's output, res [R, K] (res_dtype) the stream
  *   it joins; res_out may be NULL, or res itself (in place).  w_post and w [K]
  *   fp32; w_post may be NULL (eps_post is ignored then).  gate [gate_rows, K]

@@ -249,6 +249,28 @@ def test_infinite_and_nan_sums(name):
     assert (y[:, 1] == low[name]).all() if name in low else np.isnan(y[:, 1]).all()
 
 
+@pytest.mark.parametrize("R", [2, 16, 40, 200, 700])
+def test_int8_scales_at_the_ends_of_their_types(R):
+    """A weight scale that is infinite makes its row's results infinite, as the formula
+    does, and no other; scales of fp16's and fp32's subnormals count."""
+    N, K, nb = 140, 160, 5
+    q, qx = np.ones((N, nb, 32), np.int8), np.ones((R, K), np.int8)
+    d = np.ones((N, nb), np.float16)
+    d[3, 2], d[130, 4] = np.inf, -np.inf
+    d[64] = 2.0 ** -24
+    dx = np.ones((R, nb), np.float32)
+    dx[R - 1] = 2.0 ** -120
+    W = to_gpu(fm.pack("q8_0", {"q": q, "d": d}, N, K))
+    want = 32.0 * (dx.astype(np.float64) @ d.T.astype(np.float64))  # exact in fp32
+    y = qmoe.linear("q8", W, N, K, to_gpu(qx), to_gpu(dx))
+    assert np.array_equal(to_np(y), want.astype(np.float32))
+    y = qmoe.glu("q8", W, W, N, K, to_gpu(qx), to_gpu(dx), act=None, bias_up=to_gpu(
+        np.full(N, 1.0, np.float32)))
+    f = want.astype(np.float32)
+    one = f + np.float32(1)  # integers and tiny values: one rounding
+    assert np.array_equal(to_np(y), f * one)
+
+
 # ------------------------------------------ rows, marks, aliases, addresses --
 
 @pytest.mark.parametrize("R", [1, 16, 40, 300])
