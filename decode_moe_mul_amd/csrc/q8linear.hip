@@ -39,9 +39,8 @@ QMOE_D i32x4_t i8_mma(i32x4_t a, i32x4_t b) {  // 16 x 16 x 64
 }
 
 // ------------------------------------------------------ few rows ------
-// A block computes 16 NB weight rows (of each product) x all activation rows, 16 at
-// most; its waves split K in turns of 256 values (a pair: 128), and their sums meet in LDS in wave
-// order.  Lane 16 g + i takes 16 bytes at 16 g of every 64 of weight row i and of
+// A block computes 16 NB weight rows (of each product) x 16 activation rows; its waves
+// split K in turns of 256 values (a pair: 128), and their sums meet in LDS in wave order.  Lane 16 g + i takes 16 bytes at 16 g of every 64 of weight row i and of
 // activation row i, so that a load reads 64 consecutive bytes of 16 rows.  An op over
 // 64 values mixes two blocks: it is done twice, with the activations of either block
 // zeroed, which lanes 0..31 and 32..63 hold.
@@ -58,7 +57,9 @@ __global__ __launch_bounds__(64 * (q8_waves<GLU, NB>())) void q8_rows_kernel(Q8P
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int nb = P.K >> 5, turns = (nb + TURN - 1) / TURN, full = nb / TURN;
-  const int n0 = blockIdx.x * 16 * NB;
+  const int across = (P.N + 16 * NB - 1) / (16 * NB);  // blocks to 16 activation rows
+  const int n0 = (int)(blockIdx.x % across) * 16 * NB;
+  const int r = (int)(blockIdx.x / across) * 16 + i;  // the lane's activation row
   size_t wrow[NB], drow[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(64 * (q8_waves<GLU, NB>())) void q8_rows_kernel(Q8P
     for (int j = 0; j < 4; ++j)  // the rows of the lane's results
       drow[b][j] = (size_t)min(n0 + 16 * b + 4 * g + j, P.N - 1) * nb;
   }
-  const int xi = min(i, P.R - 1);
+  const int xi = min(r, P.R - 1);
   const int8_t* const xq = P.xq + (size_t)xi * P.K;
   const float* const xd = P.xd + (size_t)xi * nb;
   f32x4_t acc[A];
@@ -148,13 +149,16 @@ __global__ __launch_bounds__(64 * (q8_waves<GLU, NB>())) void q8_rows_kernel(Q8P
     for (int j = 0; j < 4; ++j) v[b][j] = acc[b][j], up[j] = GLU ? acc[A - NB + b][j] : 0.f;
     if constexpr (GLU) join4(P.e, v[b], up, n, P.N);
   }
-  if constexpr (NB == 2) leave_block<kOutQ8>(P.e, v[0], v[1], i, P.R, n0, P.N, g);
-  else if (i < P.R) leave4<GLU>(P.e, v[0], (size_t)i, n0 + 4 * g, P.N);
+  if constexpr (NB == 2) leave_block<kOutQ8>(P.e, v[0], v[1], r, P.R, n0, P.N, g);
+  else if (r < P.R) leave4<GLU>(P.e, v[0], (size_t)r, n0 + 4 * g, P.N);
 }
 
+static long long rows_blocks(const Q8Product& P, int cols) {
+  return (long long)((P.N + cols - 1) / cols) * ((P.R + 15) / 16);
+}
 template <bool GLU, int NB>
 static int launch_rows(const Q8Product& P, hipStream_t s) {
-  const dim3 grid((unsigned)((P.N + 16 * NB - 1) / (16 * NB)));
+  const dim3 grid((unsigned)(rows_blocks(P, 16 * NB)));
   const int waves = std::min(q8_waves<GLU, NB>(), (P.K / 32 + q8_turn<GLU>() - 1) / q8_turn<GLU>());
   return QMOE_LAUNCH("q8_rows", (q8_rows_kernel<GLU, NB>), grid, 64 * waves, 0, s, P);
 }
@@ -426,31 +430,41 @@ static int run(const ProductCall& c, hipStream_t s) {
                     (const int8_t*)w2 + L.off[0], (const uint16_t*)(w2 + L.off[1]),
                     (const int8_t*)c.codes, (const float*)c.scales, c.N, c.K, c.R,
                     epilogue_of(c)};
-  // Which kernel: as measured (us; tiles at K = 4096).
-  //   rows  16 x 4096 (K = 14336): 20.6
-  //   32 x 128, three teams  a round of tiles: 30
+  // Which kernel: as measured (us).  Both kinds go with K, so the choice does without it:
+  // rounds of blocks times the time of one at K = 4096.
+  //   rows  a round 13 (two blocks to a unit), of one block a unit 8; pairs 10.2 (one to a
+  //     unit), quantized 19.  49 x 535 (K = 3264) 7.1, with tiles 26.9; 64 x 4096 26.3, tiles
+  //     30.7; 128 x 4096 50.4, tiles 30.8; 48 x 2048 (K = 14336) 37.8, tiles 105; pairs of
+  //     64 x 2048 (K = 7168) 33.3, tiles 54.4; of 128 x 2048 64.7, tiles 55.0
+  //   32 x 128, three teams  a round of tiles 30
   //   64 x 128, two teams    37
   //   64 x 128               two to a unit 65, one 50
   //   128 x 128              two to a unit 109, one 75
-  if (P.R <= 16) {
-    if constexpr (GLU)
-      if (P.e.out == kOutQ8) return launch_rows<true, 2>(P, s);
-    return launch_rows<GLU, 1>(P, s);
-  }
+  const int cus = std::max(1, cu_count());
+  const bool wide = GLU && P.e.out == kOutQ8;
+  const long long blocks = rows_blocks(P, wide ? 32 : 16);
+  const long long round = GLU ? cus : 2LL * cus, left = blocks % round;
+  const float each = wide ? 19.f : GLU ? 10.2f : 13.f;
+  float least = each * (float)(blocks / round) + (left == 0 ? 0.f : GLU || left > cus ? each : 8.f);
   static constexpr Q8Choice choices[] = {q8_choice<Q8Tile<1, 2, 1, 2, 3>, GLU>(1, 30.f, 30.f),
                                          q8_choice<Q8Tile<2, 2, 1, 2, 2>, GLU>(1, 37.f, 37.f),
                                          q8_choice<Q8Tile<2, 2, 1, 2, 1>, GLU>(2, 65.f, 50.f),
                                          q8_choice<Q8Tile<2, 2, 2, 2, 1>, GLU>(2, 109.f, 75.f)};
-  const int cus = std::max(1, cu_count());
   const Q8Choice* best = nullptr;
-  float least = 0.f;
+  bool rows = blocks <= 0xFFFFFFFFLL / 1024;
   for (const Q8Choice& q : choices) {
+    if (rows && P.R <= 16) break;
     const long long tiles = (long long)((P.R + q.bm - 1) / q.bm) * ((P.N + q.cols - 1) / q.cols);
     if (tiles > 0xFFFFFFFFLL / q.threads) continue;
     const long long at_once = (long long)q.slots * cus, last = tiles % at_once;
     const float us = q.us * (float)(tiles / at_once) +
                      (last == 0 ? 0.f : last <= cus ? q.alone : q.us);
-    if (!best || us < least) best = &q, least = us;
+    if ((!best && !rows) || us < least) best = &q, least = us, rows = false;
+  }
+  if (rows) {
+    if constexpr (GLU)
+      if (wide) return launch_rows<true, 2>(P, s);
+    return launch_rows<GLU, 1>(P, s);
   }
   if (!best) return fail(QMOE_ERR_UNSUPPORTED, "%s: R=%d N=%d: too many tiles", c.who, c.R, c.N);
   return best->launch(P, s);

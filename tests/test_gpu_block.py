@@ -249,26 +249,31 @@ def test_infinite_and_nan_sums(name):
     assert (y[:, 1] == low[name]).all() if name in low else np.isnan(y[:, 1]).all()
 
 
-@pytest.mark.parametrize("R", [2, 16, 40, 200, 700])
-def test_int8_scales_at_the_ends_of_their_types(R):
+# few rows in one and in several groups, then every int8 tile
+@pytest.mark.parametrize("R,N", [(2, 140), (16, 140), (40, 140), (100, 4160), (300, 2008),
+                                 (700, 2600), (1000, 3900), (2000, 4003)])
+def test_int8_scales_at_the_ends_of_their_types(R, N):
     """A weight scale that is infinite makes its row's results infinite, as the formula
-    does, and no other; scales of fp16's and fp32's subnormals count."""
-    N, K, nb = 140, 160, 5
+    does, and no other; a marked block makes its row NaN; scales of fp16's and fp32's
+    subnormals count."""
+    K, nb = 160, 5
     q, qx = np.ones((N, nb, 32), np.int8), np.ones((R, K), np.int8)
     d = np.ones((N, nb), np.float16)
     d[3, 2], d[130, 4] = np.inf, -np.inf
     d[64] = 2.0 ** -24
     dx = np.ones((R, nb), np.float32)
     dx[R - 1] = 2.0 ** -120
+    dx[0, nb - 1] = np.nan
     W = to_gpu(fm.pack("q8_0", {"q": q, "d": d}, N, K))
     want = 32.0 * (dx.astype(np.float64) @ d.T.astype(np.float64))  # exact in fp32
+    assert np.isnan(want[0]).all() and not np.isnan(want[1:]).any()
     y = qmoe.linear("q8", W, N, K, to_gpu(qx), to_gpu(dx))
-    assert np.array_equal(to_np(y), want.astype(np.float32))
+    assert np.array_equal(to_np(y), want.astype(np.float32), equal_nan=True)
     y = qmoe.glu("q8", W, W, N, K, to_gpu(qx), to_gpu(dx), act=None, bias_up=to_gpu(
         np.full(N, 1.0, np.float32)))
     f = want.astype(np.float32)
     one = f + np.float32(1)  # integers and tiny values: one rounding
-    assert np.array_equal(to_np(y), f * one)
+    assert np.array_equal(to_np(y), f * one, equal_nan=True)
 
 
 # ------------------------------------------ rows, marks, aliases, addresses --
@@ -321,6 +326,27 @@ def test_quantized_output_behind_the_last_row(R, fmt):
     N, K = 160, 288
     (Wg, Wu), c, s = _real(fmt, R, N, K, 11, pair=True)
     args = (fmt, to_gpu(Wg), to_gpu(Wu), N, K, to_gpu(c), to_gpu(s))
+    want = qmoe.glu_act(*args)
+    big = [torch.full((R + 2,) + t.shape[1:], 77, dtype=t.dtype, device="cuda") for t in want]
+    qmoe.glu_act(*args, out=(big[0][:R], big[1][:R]))
+    for b, t in zip(big, want):
+        assert torch.equal(b[:R], t) and (b[R:] == 77).all()
+
+
+# int8 products: rows in one group of 16 and in several, and every tile, whose turn comes at
+# these sizes on 256 units (linear's, then pairs')
+@pytest.mark.parametrize("R,N", [(49, 535), (130, 2112), (300, 2016), (700, 2624), (1000, 3904),
+                                 (2000, 4000), (100, 2080), (300, 2080), (520, 2080)])
+def test_int8_choice_of_kernel(R, N):
+    K = 416
+    test_linear_on_an_exact_grid(R, N, K, "q8", True)
+    test_glu_on_an_exact_grid(R, N, K, "q8", False)
+    n = N // 32 * 32
+    test_glu_quantized_is_the_quantizer_on_glu(R, n, K, "q8", "silu")
+    for m in (N, N | 1):  # rows of whole pieces, and of any width
+        test_residual_in_place_and_nothing_behind_the_last_row(R, m, "q8", True)
+    (Wg, Wu), c, s = _real("q8", R, n, 288, 11, pair=True)
+    args = ("q8", to_gpu(Wg), to_gpu(Wu), n, 288, to_gpu(c), to_gpu(s))
     want = qmoe.glu_act(*args)
     big = [torch.full((R + 2,) + t.shape[1:], 77, dtype=t.dtype, device="cuda") for t in want]
     qmoe.glu_act(*args, out=(big[0][:R], big[1][:R]))
