@@ -435,7 +435,8 @@ static int run(const ProductCall& c, hipStream_t s) {
   //   rows  a round 13 (two blocks to a unit), of one block a unit 8; pairs 10.2 (one to a
   //     unit), quantized 19.  49 x 535 (K = 3264) 7.1, with tiles 26.9; 64 x 4096 26.3, tiles
   //     30.7; 128 x 4096 50.4, tiles 30.8; 48 x 2048 (K = 14336) 37.8, tiles 105; pairs of
-  //     64 x 2048 (K = 7168) 33.3, tiles 54.4; of 128 x 2048 64.7, tiles 55.0
+  //     64 x 2048 (K = 7168) 33.3, tiles 54.4; of 128 x 2048 64.7, tiles 55.0; 16 x 65536 107,
+  //     tiles 83
   //   32 x 128, three teams  a round of tiles 30
   //   64 x 128, two teams    37
   //   64 x 128               two to a unit 65, one 50
@@ -453,7 +454,7 @@ static int run(const ProductCall& c, hipStream_t s) {
   const Q8Choice* best = nullptr;
   bool rows = blocks <= 0xFFFFFFFFLL / 1024;
   for (const Q8Choice& q : choices) {
-    if (rows && P.R <= 16) break;
+    if (rows && P.R <= 4) break;  // a read of the weights: 1 x 65536 83 us, tiles 83
     const long long tiles = (long long)((P.R + q.bm - 1) / q.bm) * ((P.N + q.cols - 1) / q.cols);
     if (tiles > 0xFFFFFFFFLL / q.threads) continue;
     const long long at_once = (long long)q.slots * cus, last = tiles % at_once;

@@ -336,7 +336,8 @@ def test_quantized_output_behind_the_last_row(R, fmt):
 # int8 products: rows in one group of 16 and in several, and every tile, whose turn comes at
 # these sizes on 256 units (linear's, then pairs')
 @pytest.mark.parametrize("R,N", [(49, 535), (130, 2112), (300, 2016), (700, 2624), (1000, 3904),
-                                 (2000, 4000), (100, 2080), (300, 2080), (520, 2080)])
+                                 (2000, 4000), (100, 2080), (300, 2080), (520, 2080), (4, 26000),
+                                 (13, 26000)])
 def test_int8_choice_of_kernel(R, N):
     K = 416
     test_linear_on_an_exact_grid(R, N, K, "q8", True)
