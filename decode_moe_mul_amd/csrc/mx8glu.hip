@@ -15,34 +15,25 @@ namespace qmoe {
 template <int WR, int WC, int TM, int TN, int KS>
 using T8 = Tile<WR, WC, TM, TN, KS, true>;
 
-// Which kernel: as measured at K = 4096 with bf16 results (us; N counts the pair's
-// columns).
+// Which kernel: as measured at K = 4096 with one matrix op to a product, which now is two
+// (us; N counts the pair's columns).
 //   rows  16 x 14336: 19.8, quantized 17.7; 32 x 64: 15.3
 //   32 x 64, three teams  100 x 14336: 39.3; 64 x 64: 24.6; 128 x 64: 20.8
 //   64 x 64, two teams    333 x 2048 (K = 7168): 18.4; 32 x 64: 28.7; 128 x 64: 27.1
 //   128 x 64              700 x 2048 (K = 7168): 29; 64 x 64: 38.8; 128 x 128: 55.6
-//   128 x 128             2048 x 14336: 262-285; 128 x 64: 294; fp32 results 423, 426
-// Eight waves of 64 x 64 for the largest tile spill 120 registers: 796.
-template <bool FINE>
-static int launch(const ProductCall& c, const MxProduct& P, hipStream_t s) {
-  const int cus = std::max(1, cu_count());
-  if (P.R <= 16 && P.N <= 32 * cus) {
-    if constexpr (!FINE)
-      if (P.e.out > kOutBF16) return launch_rows<true, true, 2>("mxfp8_glu_rows", P, s);
-    return launch_rows<true, true, 1, FINE>("mxfp8_glu_rows", P, s);
-  }
-  static constexpr Choice choices[] = {choice<T8<1, 2, 1, 2, 3>, true, FINE>(1, 9.8f),
-                                       choice<T8<2, 2, 1, 2, 2>, true, FINE>(1, 11.5f),
-                                       choice<T8<2, 2, 2, 2, 1>, true, FINE>(1, FINE ? 30.4f : 20.8f),
-                                       choice<T8<2, 2, 2, 4, 1>, true, FINE>(1, FINE ? 60.f : 39.f)};
-  return launch_choice(choices, c.who, "mxfp8_glu_tile", P, s);
-}
-
+//   two ops: 2048 x 14336 423-426
 static int run(const ProductCall& c, hipStream_t s) {
   const int st = check_product(c);
   if (st) return st == kNothing ? QMOE_OK : st;
   const MxProduct P = mx_product(c);
-  return P.e.out == kOutF32 ? launch<true>(c, P, s) : launch<false>(c, P, s);
+  const int cus = std::max(1, cu_count());
+  if (P.R <= 16 && P.N <= 32 * cus)
+    return P.e.out > kOutBF16 ? launch_rows<true, true, 2>("mxfp8_glu_rows", P, s)
+                              : launch_rows<true, true, 1>("mxfp8_glu_rows", P, s);
+  static constexpr Choice choices[] = {
+      choice<T8<1, 2, 1, 2, 3>, true>(1, 9.8f), choice<T8<2, 2, 1, 2, 2>, true>(1, 11.5f),
+      choice<T8<2, 2, 2, 2, 1>, true>(1, 30.4f), choice<T8<2, 2, 2, 4, 1>, true>(1, 60.f)};
+  return launch_choice(choices, c.who, "mxfp8_glu_tile", P, s);
 }
 
 }  // namespace qmoe

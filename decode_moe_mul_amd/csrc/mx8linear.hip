@@ -5,7 +5,9 @@
 //
 // E2M1 codes against E4M3 codes, one E8M0 scale per 32 values along K on either
 // side, used as stored: every product of two codes is exact, the matrix op applies
-// both scales and accumulates in fp32.
+// both scales and accumulates in fp32.  It is issued twice, for the small and the large
+// codes, because one op drops what lies far below its largest product (split_e4m3): twice
+// the matrix work, 2048 x 4096 x 4096 from 39 to 59 us.
 #include "mxcall.hpp"
 
 #pragma clang fp contract(off)
@@ -15,32 +17,25 @@ namespace qmoe {
 template <int WR, int WC, int TM, int TN, int KS>
 using T8 = Tile<WR, WC, TM, TN, KS, true>;
 
-// Which kernel: as measured at K = 4096 with bf16 results (us).
+// Which kernel: as measured at K = 4096 with one matrix op to a product, which now is two (us).
 //   rows  1 x 4096: 3.8
 //   32 x 64, four teams    128 x 4096: 6.4; 64 x 64: 7.9; 64 x 128: 9.2
 //   64 x 64, three teams   333 x 2050 (K = 7200): 17.2; 32 x 64: 22.9; 64 x 128: 21.4
 //   64 x 128, two teams    2048 x 4096: 58.7
-//   128 x 128              2048 x 4096: 41.8;  (K = 14336) 121
-//   128 x 256              2048 x 4096: 38.9;  (K = 14336) 112; 2048 x 14336 with fp32
-//     results 243, 128 x 128: 213
+//   128 x 128              2048 x 4096: 41.8
+//   two ops: 2048 x 14336 128 x 256 243, 128 x 128 213
 // (An activation row has 256 bytes a step: LDS holds no two of the larger tiles.)
-template <bool FINE>
-static int launch(const ProductCall& c, const MxProduct& P, hipStream_t s) {
-  const int cus = std::max(1, cu_count());
-  if (P.R <= 16 && P.N <= 32 * cus) return launch_rows<true, false, 1, FINE>("mxfp8_rows", P, s);
-  static constexpr Choice choices[] = {choice<T8<1, 2, 1, 1, 4>, false, FINE>(1, 6.6f),
-                                       choice<T8<2, 2, 1, 1, 3>, false, FINE>(1, 9.5f),
-                                       choice<T8<2, 2, 1, 2, 2>, false, FINE>(1, 14.f),
-                                       choice<T8<2, 2, 2, 2, 1>, false, FINE>(1, FINE ? 30.f : 20.5f),
-                                       choice<T8<2, 2, 2, 4, 1>, false, FINE>(1, FINE ? 61.f : 38.f)};
-  return launch_choice(choices, c.who, "mxfp8_tile", P, s);
-}
-
 static int run(const ProductCall& c, hipStream_t s) {
   const int st = check_product(c);
   if (st) return st == kNothing ? QMOE_OK : st;
   const MxProduct P = mx_product(c);
-  return P.e.out == kOutF32 ? launch<true>(c, P, s) : launch<false>(c, P, s);
+  const int cus = std::max(1, cu_count());
+  if (P.R <= 16 && P.N <= 32 * cus) return launch_rows<true, false, 1>("mxfp8_rows", P, s);
+  static constexpr Choice choices[] = {
+      choice<T8<1, 2, 1, 1, 4>, false>(1, 6.6f), choice<T8<2, 2, 1, 1, 3>, false>(1, 9.5f),
+      choice<T8<2, 2, 1, 2, 2>, false>(1, 14.f), choice<T8<2, 2, 2, 2, 1>, false>(1, 30.f),
+      choice<T8<2, 2, 2, 4, 1>, false>(1, 61.f)};
+  return launch_choice(choices, c.who, "mxfp8_tile", P, s);
 }
 
 }  // namespace qmoe

@@ -23,7 +23,7 @@
 
 namespace qmoe {
 
-template <bool XF8, bool FINE>
+template <bool XF8>
 QMOE_D v4f_t mx_mma16(uint4 w, uint32_t sw, uint4 x, uint4 xhi, uint32_t sx, v4f_t c) {
   const v8i_t wv = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
   if constexpr (XF8) {
@@ -33,14 +33,10 @@ QMOE_D v4f_t mx_mma16(uint4 w, uint32_t sw, uint4 x, uint4 xhi, uint32_t sx, v4f
       return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, sum, 4, 0, 0, (int)sw, 0,
                                                               (int)sx);
     };
-    if constexpr (FINE) {
-      uint4 bl, bh, sl, sh;
-      split_e4m3(x, bl, sl);
-      split_e4m3(xhi, bh, sh);
-      return op(bl, bh, op(sl, sh, c));
-    } else {
-      return op(x, xhi, c);
-    }
+    uint4 bl, bh, sl, sh;  // as in the tiles: two ops, and no product is cut
+    split_e4m3(x, bl, sl);
+    split_e4m3(xhi, bh, sh);
+    return op(bl, bh, op(sl, sh, c));
   } else {
     const v8i_t xv = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, c, 4, 4, 0, (int)sw, 0,
@@ -89,7 +85,7 @@ QMOE_D void load_frag(const uint8_t* q, const uint8_t* s, size_t row, int b0, in
 template <bool GLU, int NB>
 constexpr int rows_waves() { return GLU && NB == 2 ? 8 : 16; }
 
-template <bool XF8, bool GLU, int NB, bool FINE>
+template <bool XF8, bool GLU, int NB>
 __global__ __launch_bounds__(64 * (rows_waves<GLU, NB>())) void mx_rows_kernel(MxProduct P) {
   constexpr int A = (GLU ? 2 : 1) * NB;  // 16 x 16 sums: gate's (or all), then up's
   __shared__ v4f_t sums[rows_waves<GLU, NB>()][A][64];
@@ -117,7 +113,7 @@ __global__ __launch_bounds__(64 * (rows_waves<GLU, NB>())) void mx_rows_kernel(M
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int a = 0; a < A; ++a)
-        acc[a] = mx_mma16<XF8, FINE>(w[a].q[j], w[a].s[j], x.q[j], x.hi[XF8 ? j : 0], x.s[j], acc[a]);
+        acc[a] = mx_mma16<XF8>(w[a].q[j], w[a].s[j], x.q[j], x.hi[XF8 ? j : 0], x.s[j], acc[a]);
   };
   int u = wave;
   for (; u < full; u += waves) turn(std::false_type{}, u);
@@ -149,11 +145,11 @@ __global__ __launch_bounds__(64 * (rows_waves<GLU, NB>())) void mx_rows_kernel(M
     leave4<GLU>(P.e, v[0], (size_t)i, n0 + 4 * g, P.N);
 }
 
-template <bool XF8, bool GLU, int NB, bool FINE = false>
+template <bool XF8, bool GLU, int NB>
 static int launch_rows(const char* name, const MxProduct& P, hipStream_t s) {
   const dim3 grid((unsigned)((P.N + 16 * NB - 1) / (16 * NB)));
   const int waves = std::min(rows_waves<GLU, NB>(), (P.K / 32 + 15) / 16);
-  return QMOE_LAUNCH(name, (mx_rows_kernel<XF8, GLU, NB, FINE>), grid, 64 * waves, 0, s, P);
+  return QMOE_LAUNCH(name, (mx_rows_kernel<XF8, GLU, NB>), grid, 64 * waves, 0, s, P);
 }
 
 }  // namespace qmoe

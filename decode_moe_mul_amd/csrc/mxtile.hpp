@@ -99,11 +99,12 @@ QMOE_D void set_op(ActOp<false>& o, uint4 lo, uint4) { o.lo = lo; }
 QMOE_D void set_op(ActOp<true>& o, uint4 lo, uint4 hi) { o.lo = lo, o.hi = hi; }
 
 // The matrix op aligns the products of eight consecutive values of MXFP8 to the
-// largest of them and drops what lies more than 13 binary places below (measured;
-// a sum of 64 N(0, 1) products is off by 4.5e-6).  Cut at the middle exponent, the
-// codes of either half span eight binary places, and every product stays: two
-// exact ops.  `small` are the codes with an exponent field below 8, `big` the
-// others, zeros of either sign in their places.
+// largest of them and drops what lies more than 13 binary places below (measured): a
+// sum of 64 N(0, 1) products is off by 4.5e-6, one beside a channel a thousand times
+// louder by 2^-9 and more, and one whose largest products cancel loses all of it.  Cut
+// at the middle exponent, the codes of either half span eight binary places, and every
+// product stays: two exact ops.  `small` are the codes with an exponent field below 8,
+// `big` the others, zeros of either sign in their places.
 QMOE_D void split_e4m3(uint4 v, uint4& big, uint4& small) {
   const auto cut = [](uint32_t w, uint32_t& b, uint32_t& s) {
     const uint32_t t = w & 0x40404040u;
@@ -132,15 +133,12 @@ QMOE_D v16f_t mx_mma32(const ActOp<XF8>& x, uint32_t sa, uint4 b, uint32_t sb, v
   }
 }
 
-// FINE: MXFP8 products without the op's loss, at twice the ops; for results in fp32.
-// (Rounded to bf16 or to codes, a result has an error a thousand times that loss.)
-template <class T, bool GLU, bool FINE>
+template <class T, bool GLU>
 __global__ __launch_bounds__(T::THREADS) void mx_tile_kernel(MxProduct P, int tiles_m,
                                                              int tiles_n) {
   constexpr int TM = T::TM, TN = T::TN, M = TM * TN, NR = TM + TN;
   constexpr bool XF8 = T::XF8;
   static_assert(!GLU || TN % 2 == 0, "");
-  static_assert(!FINE || XF8, "");
   extern __shared__ __align__(16) uint8_t smem[];
   const int team = T::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / T::TEAM);
   const int tid = threadIdx.x % T::TEAM, lane = tid & 63, i = lane & 31, h = lane >> 5;
@@ -280,11 +278,11 @@ __global__ __launch_bounds__(T::THREADS) void mx_tile_kernel(MxProduct P, int ti
   };
   // one group of ops with `side(n)` issued after the n-th
   const auto group = [&](auto sel, const Ops& o, const Scl& c, auto&& side) {
-    ActOp<FINE> small, big;  // of the row that the last op took
+    ActOp<XF8> small, big;  // MXFP8: of the row that the last op took
     static_for<M>([&](auto slot) {
       constexpr int m = decltype(slot)::value / TN, n = decltype(slot)::value % TN;
       constexpr int SEL = decltype(sel)::value;
-      if constexpr (FINE) {
+      if constexpr (XF8) {
         if constexpr (n == 0) {
           split_e4m3(o.a[m].lo, big.lo, small.lo);
           split_e4m3(o.a[m].hi, big.hi, small.hi);
@@ -426,7 +424,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_tile_kernel(MxProduct P, int ti
   });
 }
 
-template <class T, bool GLU, bool FINE>
+template <class T, bool GLU>
 static int launch_tile(const char* name, const MxProduct& P, hipStream_t s) {
   constexpr int cols = GLU ? T::BN / 2 : T::BN;
   const int tm = (P.R + T::BM - 1) / T::BM, tn = (P.N + cols - 1) / cols;
@@ -437,11 +435,11 @@ static int launch_tile(const char* name, const MxProduct& P, hipStream_t s) {
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) dev = 64;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!bit || !(declared.load(std::memory_order_relaxed) & bit)) {
-    (void)hipFuncSetAttribute((const void*)mx_tile_kernel<T, GLU, FINE>,
+    (void)hipFuncSetAttribute((const void*)mx_tile_kernel<T, GLU>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)T::LDS);
     declared.fetch_or(bit, std::memory_order_relaxed);
   }
-  return QMOE_LAUNCH(name, (mx_tile_kernel<T, GLU, FINE>), grid, T::THREADS, T::LDS, s, P, tm, tn);
+  return QMOE_LAUNCH(name, (mx_tile_kernel<T, GLU>), grid, T::THREADS, T::LDS, s, P, tm, tn);
 }
 
 struct Choice {
@@ -449,10 +447,10 @@ struct Choice {
   float us, alone;
   int (*launch)(const char*, const MxProduct&, hipStream_t);
 };
-template <class T, bool GLU, bool FINE = false>
+template <class T, bool GLU>
 static constexpr Choice choice(int slots, float us, float alone = 0.f) {
   return {T::BM, GLU ? T::BN / 2 : T::BN, T::THREADS, slots, us, alone > 0.f ? alone : us,
-          launch_tile<T, GLU, FINE>};
+          launch_tile<T, GLU>};
 }
 
 // A round of tiles takes about as long as one tile, so with K given the choice

@@ -790,7 +790,7 @@ def glu(fmt, Wg, Wu, N, K, codes, scales, act="silu", bias_gate=None, bias_up=No
 
 def glu_act(fmt, Wg, Wu, N, K, codes, scales, act="silu", bias_gate=None, bias_up=None, out=None):
     """glu's float32 rows as activations (codes, scales) of the next product, in
-    the same format fmt."""
+    the same format fmt (the sums may be in another order than glu's)."""
     _th or _load_torch()
     R, index, code = _product_args(fmt, N, K, codes, scales, act, Wg, Wu)
     bg, bu = _bias(bias_gate, N, index, "bias_gate"), _bias(bias_up, N, index, "bias_up")

@@ -481,12 +481,10 @@ int qgemm_mxfp4_mxfp4(const void *W, int N, int K, const uint8_t *codes,
  * W, Wg, Wu [N, K] in qmoe layout, 256-byte aligned; activations as the
  * quantizers, qnorm_act_*, qnorm_block_act_*, qswiglu_act_* and qglu_*_act
  * write them, codes 16-byte aligned (d: 4, E8M0 scales: any).  Products of codes
- * are exact, of q8 the sums over a 32-value block too; sums are fp32 from there.
- * (mxfp8 with a result in bf16 or in codes: of eight consecutive products, what
- * lies more than 13 binary places below the largest is dropped, 4.5e-6 of a sum of
- * normal values and at most 2^-10 sum |w x|; with a result in fp32 nothing is.)
- * The kernel that R and N call for may sum in another order, so a row's last
- * bits can depend on R.
+ * are exact, of q8 the sums over a 32-value block too; sums are fp32 from there,
+ * whatever the result's type.  The kernel that R and N call for may sum in another
+ * order, so a row's last bits can depend on R; qglu_<fmt>_act may also sum in another
+ * order than qglu_<fmt>.
  *
  * qlinear_<fmt>: y [R, N] (y_dtype) = act( sum_k w[n, k] x[r, k] + bias[n] )
  *                                     + res[r, n]
@@ -496,8 +494,9 @@ int qgemm_mxfp4_mxfp4(const void *W, int N, int K, const uint8_t *codes,
  *     act( sum_k wg[n, k] x[r, k] + bias_gate[n] )
  *     * ( sum_k wu[n, k] x[r, k] + bias_up[n] )
  *   bias_gate, bias_up [N] fp32 or NULL.
- * qglu_<fmt>_act: the activation quantizer of <fmt> applied to qglu's fp32 y
- *   (N % 32 == 0; scales at any address, out_d 4-byte aligned).  A block with
+ * qglu_<fmt>_act: the activation quantizer of <fmt> applied to an fp32 y as qglu's
+ *   (N % 32 == 0; scales at any address, out_d 4-byte aligned; where the order of
+ *   its sums is another, a value next to a border can have the neighbouring code).  A block with
  *   a NaN or an infinity is marked as in the section above.
  *   act is a qmoe_act.  Everything after the sums is fp32, with exponentials
  *   and reciprocals of the hardware: an activation of v is within 2^-20
