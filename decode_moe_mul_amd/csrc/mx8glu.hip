@@ -15,13 +15,13 @@ namespace qmoe {
 template <int WR, int WC, int TM, int TN, int KS>
 using T8 = Tile<WR, WC, TM, TN, KS, true>;
 
-// Which kernel: as measured at K = 4096 with one matrix op to a product, which now is two
-// (us; N counts the pair's columns).
-//   rows  16 x 14336: 19.8, quantized 17.7; 32 x 64: 15.3
-//   32 x 64, three teams  100 x 14336: 39.3; 64 x 64: 24.6; 128 x 64: 20.8
-//   64 x 64, two teams    333 x 2048 (K = 7168): 18.4; 32 x 64: 28.7; 128 x 64: 27.1
-//   128 x 64              700 x 2048 (K = 7168): 29; 64 x 64: 38.8; 128 x 128: 55.6
-//   two ops: 2048 x 14336 423-426
+// Which kernel: as measured at K = 4096 with bf16 results (us; N counts the pair's
+// columns; every product is two matrix ops, as in qlinear_mxfp8).
+//   32 x 64, three teams  64 x 2048 (K = 7168): 17.9; 64 x 64: 23.3; 128 x 64: 45.5
+//   64 x 64, two teams    333 x 2048 (K = 7168): 24.6; 32 x 64: 36.4; 128 x 64: 45.4
+//   128 x 64              700 x 2048 (K = 7168): 46.0; 64 x 64: 48.6
+//                         2048 x 14336: 407, 64 x 64: 466; quantized 416, fp32 416
+// 128 x 128 takes 418 there, two of 128 x 64's rounds everywhere: it is not here.
 static int run(const ProductCall& c, hipStream_t s) {
   const int st = check_product(c);
   if (st) return st == kNothing ? QMOE_OK : st;
@@ -30,9 +30,9 @@ static int run(const ProductCall& c, hipStream_t s) {
   if (P.R <= 16 && P.N <= 32 * cus)
     return P.e.out > kOutBF16 ? launch_rows<true, true, 2>("mxfp8_glu_rows", P, s)
                               : launch_rows<true, true, 1>("mxfp8_glu_rows", P, s);
-  static constexpr Choice choices[] = {
-      choice<T8<1, 2, 1, 2, 3>, true>(1, 9.8f), choice<T8<2, 2, 1, 2, 2>, true>(1, 11.5f),
-      choice<T8<2, 2, 2, 2, 1>, true>(1, 30.4f), choice<T8<2, 2, 2, 4, 1>, true>(1, 60.f)};
+  static constexpr Choice choices[] = {choice<T8<1, 2, 1, 2, 3>, true>(1, 12.f),
+                                       choice<T8<2, 2, 1, 2, 2>, true>(1, 16.3f),
+                                       choice<T8<2, 2, 2, 2, 1>, true>(1, 29.3f)};
   return launch_choice(choices, c.who, "mxfp8_glu_tile", P, s);
 }
 
