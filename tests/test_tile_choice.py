@@ -46,3 +46,16 @@ def test_every_tile_is_the_choice_somewhere(name, pair):
             times = [_rounds(c, R, N) for c in choices]
             won.add(times.index(min(times)))
     assert won == set(range(len(choices)))
+
+
+def test_the_sums_over_long_k_are_tested_with_every_tile():
+    pytest.importorskip("torch")
+    from test_gpu_block_long import TILES
+    files = {"mxfp4": ("mx4gemm.hip", "mx4glu.hip"), "mxfp8": ("mx8linear.hip", "mx8glu.hip"),
+             "q8": ("q8linear.hip", "q8linear.hip")}
+    for (fmt, pair), sizes in TILES.items():
+        choices = _choices(files[fmt][pair], pair)
+        assert len(sizes) == len(choices)
+        for i, (_, R, N) in enumerate(sizes):
+            times = [_rounds(c, R, N) for c in choices]
+            assert times.index(min(times)) == i
