@@ -41,9 +41,10 @@ QMOE_D float recip(float v) { return __builtin_amdgcn_rcpf(v); }
 
 // Phi(-|v|) of the normal distribution: half of erfc(z), z = |v| / sqrt 2, as
 // t exp(-z^2) P(t), t = 1 / (1 + 0.4 z).  P of degree 8 is fitted to
-// exp(z^2) erfc(z) / t over all z >= 0 (minimax by reweighted least squares;
-// relative error 1.3e-7), so the tail keeps its relative precision, which
-// 1 + erf would lose.  15 instructions; a library erfc takes 40 with a branch.
+// exp(z^2) erfc(z) / t over all z >= 0 (reweighted least squares; with the
+// coefficients as they stand here its relative error is at most 1.6e-7),
+// so the tail keeps its relative precision, which 1 + erf would lose.  15
+// instructions; a library erfc takes 40 with a branch.
 QMOE_D float normal_tail(float v) {
   const float t = recip(fmaf(fabsf(v), 0.28284271247f, 1.f));
   float p = 0.05025659129023552f;
