@@ -35,7 +35,11 @@ struct Epilogue {
 };
 
 // exp through the hardware's exp2: the product with log2 e is rounded, so the
-// relative error grows with |v|: |v| 2^-24 on top of exp2's own
+// relative error grows with |v|: |v| 2^-24 on top of exp2's own.  (Of normal values
+// silu is off by 4.7e-8 in the mean square, gelu_tanh by 4.7e-8, as against 3.9e-8 and
+// 4.2e-8 with torch's exp and division.  A Newton step on the reciprocal and the
+// product's remainder in the exponent make it 4.5e-8 and 4.6e-8, and a pair of
+// 2048 x 14336 x 4096 in MXFP4 169 to 172 us instead of 162.)
 QMOE_D float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.4426950408889634f); }
 QMOE_D float recip(float v) { return __builtin_amdgcn_rcpf(v); }
 
@@ -130,7 +134,6 @@ QMOE_D void leave4(const Epilogue& e, float (&v)[4], size_t row, int n, int N) {
       if (n + j < N) store_at(e, at + j, v[j]);
   }
 }
-
 
 // A gated pair's four columns n .. n + 3: v = act(v + bias) * (up + bias2).
 QMOE_D void join4(const Epilogue& e, float (&v)[4], const float (&up)[4], int n, int N) {
@@ -235,7 +238,8 @@ struct Leave {
   template <Res RES, int OUT>
   struct Residual {  // of a lane's pieces of 32 rows, four columns to an element
     static constexpr int H = Piece<OUT>::E / 4;
-    typename std::conditional<RES == kBF16, u32x2, u32x4>::type v[RES == kNone ? 1 : Piece<OUT>::Z * H];
+    typename std::conditional<RES == kBF16, u32x2, u32x4>::type
+        v[RES == kNone ? 1 : Piece<OUT>::Z * H];
   };
   // the residual of rows row0 .. + 31, all pieces at once: one wait for memory
   template <Res RES, int OUT>

@@ -40,7 +40,8 @@ QMOE_D i32x4_t i8_mma(i32x4_t a, i32x4_t b) {  // 16 x 16 x 64
 
 // ------------------------------------------------------ few rows ------
 // A block computes 16 NB weight rows (of each product) x 16 activation rows; its waves
-// split K in turns of 256 values (a pair: 128), and their sums meet in LDS in wave order.  Lane 16 g + i takes 16 bytes at 16 g of every 64 of weight row i and of
+// split K in turns of 256 values (a pair: 128), and their sums meet in LDS in wave
+// order.  Lane 16 g + i takes 16 bytes at 16 g of every 64 of weight row i and of
 // activation row i, so that a load reads 64 consecutive bytes of 16 rows.  An op over
 // 64 values mixes two blocks: it is done twice, with the activations of either block
 // zeroed, which lanes 0..31 and 32..63 hold.
@@ -174,7 +175,8 @@ static int launch_rows(const Q8Product& P, hipStream_t s) {
 // one after the other 112-147.  The fp32 op takes 64 cycles of the vector unit's own (a
 // probe: it and 16 multiply-adds take the sum of both, the integer op hides behind
 // them), about 211 a pair of ops in all; the scales as a bf16 op of their parts, which
-// does overlap, gained 2 %, because waits for copies and barriers are 38 % of a wave.
+// does overlap, gained 2 %, because waits for copies and barriers are 38 % of a wave
+// (the loop over steps says which).
 //
 // K advances 128 values (four blocks) a step.  Codes go from memory to LDS without
 // passing registers, whole 128-byte lines, into one of two buffers, a step ahead;
@@ -204,8 +206,8 @@ struct Q8Tile {
 // (Two waves to a SIMD leave a wave 256 registers, all of which the vector unit reads;
 // with 512 the compiler puts the ops' results where it does not and copies each.)
 template <class T, bool GLU>
-__global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_kernel(Q8Product P, int tiles_m,
-                                                             int tiles_n) {
+__global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_kernel(
+    Q8Product P, int tiles_m, int tiles_n) {
   constexpr int TM = T::TM, TN = T::TN, M = TM * TN;
   extern __shared__ __align__(16) uint8_t smem[];
   const int team = T::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / T::TEAM);
@@ -243,7 +245,8 @@ __global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_
     const int8_t* base = j < T::JA ? abase : bbase;
     if (GLU && j >= T::JA && ((wave + T::NW * (j - T::JA)) >> 2 & 1)) base = bbase2;
     copy_to_lds(lds0 + (st & 1) * T::BUF + (wave + T::NW * j) * 1024,
-                uniform((const uint8_t*)base + (size_t)k * 128), off[j] - (k + 1 == all ? over : 0));
+                uniform((const uint8_t*)base + (size_t)k * 128),
+                off[j] - (k + 1 == all ? over : 0));
   };
   f32x4_t sreg[T::SC];
   const auto load_scales = [&](int st) {
@@ -280,7 +283,9 @@ __global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_
     });
   };
   const int wm = (wave / T::WC) * 32 * TM, wn = (wave % T::WC) * 32 * TN;
-  const auto row_of = [&](int r) { return r < TM ? wm + 32 * r + i : T::BM + wn + 32 * (r - TM) + i; };
+  const auto row_of = [&](int r) {
+    return r < TM ? wm + 32 * r + i : T::BM + wn + 32 * (r - TM) + i;
+  };
   f32x16_t acc[TM][TN];
 #pragma unroll
   for (int m = 0; m < TM; ++m)
@@ -300,7 +305,8 @@ __global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_
     f32x16_t sum[2], mul[2];
     const auto read = [&](auto b) {
       static_for<TM + TN>([&](auto r) {
-        q[b & 1][r] = *(const i32x4_t*)(buf + row_of(r) * 128 + 16 * ((2 * b + h) ^ ((i >> 1) & 7)));
+        q[b & 1][r] =
+            *(const i32x4_t*)(buf + row_of(r) * 128 + 16 * ((2 * b + h) ^ ((i >> 1) & 7)));
       });
     };
     const auto sums = [&](auto t) {
@@ -340,9 +346,13 @@ __global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  // Buffer st & 1 holds step st; the next step's codes are on their way to the other,
-  // the scales of the one after it in registers.  What is fetched past a team's steps
-  // repeats the last one and is not used.
+  // Buffer st & 1 holds step st.  A step asks for the next one's codes, stores that one's
+  // scales and loads those of the one after it, then computes.  Vector loads return in
+  // order and the compiler does not count the copies, so its waits for the scales (before
+  // they are stored, before they are made fp32) are waits for the step's copies too: a
+  // wave's arithmetic begins when they have come, and what runs meanwhile is the other
+  // block on the unit, where there is one.  What is fetched past a team's steps repeats
+  // the last one and is not used.
   static_for<T::J>([&](auto j) { copy(0, j); });
   load_scales(0);
   store_scales(0);
@@ -366,7 +376,8 @@ __global__ __launch_bounds__(T::THREADS, T::THREADS > 256 ? 1 : 2) void q8_tile_
       for (int n = 0; n < TN; ++n)
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (team > 0) sums[((team - 1) * M * 16 + (m * TN + n) * 16 + j) * T::TEAM] = acc[m][n][j];
+          if (team > 0)
+            sums[((team - 1) * M * 16 + (m * TN + n) * 16 + j) * T::TEAM] = acc[m][n][j];
     __syncthreads();
     if (team > 0) return;
 #pragma unroll 1
@@ -432,11 +443,12 @@ static int run(const ProductCall& c, hipStream_t s) {
                     epilogue_of(c)};
   // Which kernel: as measured (us).  Both kinds go with K, so the choice does without it:
   // rounds of blocks times the time of one at K = 4096.
-  //   rows  a round 13 (two blocks to a unit), of one block a unit 8; pairs 10.2 (one to a
-  //     unit), quantized 19.  49 x 535 (K = 3264) 7.1, with tiles 26.9; 64 x 4096 26.3, tiles
-  //     30.7; 128 x 4096 50.4, tiles 30.8; 48 x 2048 (K = 14336) 37.8, tiles 105; pairs of
-  //     64 x 2048 (K = 7168) 33.3, tiles 54.4; of 128 x 2048 64.7, tiles 55.0; 16 x 65536 107,
-  //     tiles 83
+  //   rows  two blocks a unit 13, one 8, pairs 10.2 a block, quantized 19; a unit takes
+  //     its blocks one after the other (from K = 4096 on 16 waves of 128 registers fill
+  //     it).  49 x 535 (K = 3264) 7.1, with tiles 26.9; 64 x 4096 26.3, tiles 30.7;
+  //     128 x 4096 50.4, tiles 30.8; 48 x 2048 (K = 14336) 37.8, tiles 105; pairs of
+  //     64 x 2048 (K = 7168) 33.3, tiles 54.4; of 128 x 2048 64.7, tiles 55.0; 16 x 65536
+  //     107, tiles 83
   //   32 x 128, three teams  a round of tiles 30
   //   64 x 128, two teams    37
   //   64 x 128               two to a unit 65, one 50

@@ -65,9 +65,10 @@ def test_products_over_many_turns(fmt, pair, R, N, K):
     assert (x.abs() @ w[0].abs().t()).max() < 2.0 ** (22 if fmt == "q8" else 20)
     sums = [x @ v.t() for v in w]
     W, c, s = [to_gpu(v) for v in W], to_gpu(c), to_gpu(s)
-    # the oracle's own sums, in 64 bits, of the last rows and columns
+    # the same in 64 bits for the last rows and columns
     r, n = min(R, 5), min(N, 9)
-    assert torch.equal(sums[0][R - r:, N - n:].double(), x[R - r:].double() @ w[0][N - n:].double().t())
+    want = x[R - r:].double() @ w[0][N - n:].double().t()
+    assert torch.equal(sums[0][R - r:, N - n:].double(), want)
     del x, w
     if not pair:
         assert torch.equal(qmoe.linear(fmt, W[0], N, K, c, s), sums[0])
