@@ -22,6 +22,8 @@ using T8 = Tile<WR, WC, TM, TN, KS, true>;
 //   128 x 64              700 x 2048 (K = 7168): 46.0; 64 x 64: 48.6
 //                         2048 x 14336: 407, 64 x 64: 466; quantized 416, fp32 416
 // 128 x 128 takes 418 there, two of 128 x 64's rounds everywhere: it is not here.
+// Against the best of the three for R from 40 to 2048, N from 2048 to 14336 and K from
+// 1024 to 14336 (51 sizes) the choice takes at most 6 % longer.
 static int run(const ProductCall& c, hipStream_t s) {
   const int st = check_product(c);
   if (st) return st == kNothing ? QMOE_OK : st;

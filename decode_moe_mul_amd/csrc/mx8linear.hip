@@ -25,6 +25,8 @@ using T8 = Tile<WR, WC, TM, TN, KS, true>;
 //   128 x 128              2048 x 4096: 58.7; 2048 x 14336: 202, 64 x 128: 235
 // 128 x 256 takes 61.1 and 233, two of 128 x 128's rounds and more: it is not here.
 // (An activation row has 256 bytes a step: LDS holds no two of the largest tile.)
+// Against the best of the four for R from 40 to 2048, N from 2048 to 14336 and K from
+// 1024 to 14336 (51 sizes) the choice takes at most 7 % longer.
 static int run(const ProductCall& c, hipStream_t s) {
   const int st = check_product(c);
   if (st) return st == kNothing ? QMOE_OK : st;
