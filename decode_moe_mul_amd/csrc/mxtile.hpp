@@ -104,13 +104,13 @@ QMOE_D void set_op(ActOp<true>& o, uint4 lo, uint4 hi) { o.lo = lo, o.hi = hi; }
 // louder by 2^-9 and more, and one whose largest products cancel loses all of it.  Cut
 // at the middle exponent, the codes of either half span eight binary places, and every
 // product stays: two exact ops.  `small` are the codes with an exponent field below 8,
-// `big` the others, zeros of either sign in their places.
+// `big` the others, zeros in their places.
 QMOE_D void split_e4m3(uint4 v, uint4& big, uint4& small) {
   const auto cut = [](uint32_t w, uint32_t& b, uint32_t& s) {
-    const uint32_t t = w & 0x40404040u;
-    const uint32_t m = (t << 1) - (t >> 6);  // 0x7F in the bytes of large codes
-    b = w & (m | 0x80808080u);
-    s = w & ~m;
+    // 0xFF in the bytes of large codes (bit 6 set): the permute repeats the top bits of
+    // the odd bytes of its two sources, w moved up by a bit and by a byte and a bit
+    b = w & __builtin_amdgcn_perm(w << 9, w << 1, 0x090B080Au);
+    s = w ^ b;
   };
   cut(v.x, big.x, small.x);
   cut(v.y, big.y, small.y);
