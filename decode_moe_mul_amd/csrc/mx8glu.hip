@@ -17,11 +17,11 @@ using T8 = Tile<WR, WC, TM, TN, KS, true>;
 
 // Which kernel: as measured at K = 4096 with bf16 results (us; N counts the pair's
 // columns; every product is two matrix ops, as in qlinear_mxfp8).
-//   32 x 64, three teams  64 x 2048 (K = 7168): 17.9; 64 x 64: 23.3; 128 x 64: 45.5
-//   64 x 64, two teams    333 x 2048 (K = 7168): 24.6; 32 x 64: 36.4; 128 x 64: 45.4
-//   128 x 64              700 x 2048 (K = 7168): 46.0; 64 x 64: 48.6
-//                         2048 x 14336: 407, 64 x 64: 466; quantized 416, fp32 416
-// 128 x 128 takes 418 there, two of 128 x 64's rounds everywhere: it is not here.
+//   32 x 64, three teams  64 x 2048 (K = 7168): 17.1; 64 x 64: 22.0; 128 x 64: 42.2
+//   64 x 64, two teams    333 x 2048 (K = 7168): 24.4; 32 x 64: 35.8; 128 x 64: 42.3
+//   128 x 64              700 x 2048 (K = 7168): 44.3; 64 x 64: 48.6
+//                         2048 x 14336: 422, 64 x 64: 478; quantized 421, fp32 428
+// 128 x 128 takes two of 128 x 64's rounds (3 % more at 2048 x 14336): it is not here.
 // Against the best of the three for R from 40 to 2048, N from 2048 to 14336 and K from
 // 1024 to 14336 (51 sizes) the choice takes at most 6 % longer.
 static int run(const ProductCall& c, hipStream_t s) {

@@ -7,7 +7,7 @@
 // side, used as stored: every product of two codes is exact, the matrix op applies
 // both scales and accumulates in fp32.  It is issued twice, for the small and the large
 // codes, because one op drops what lies far below its largest product (split_e4m3): twice
-// the matrix work, 2048 x 4096 x 4096 from 39 to 59 us.
+// the matrix work, 2048 x 4096 x 4096 from 39 to 62 us.
 #include "mxcall.hpp"
 
 #pragma clang fp contract(off)
@@ -17,13 +17,15 @@ namespace qmoe {
 template <int WR, int WC, int TM, int TN, int KS>
 using T8 = Tile<WR, WC, TM, TN, KS, true>;
 
-// Which kernel: as measured at K = 4096 with bf16 results (us; fp32 takes up to 2 % more).
+// Which kernel: as measured at K = 4096 with bf16 results (us; fp32 takes up to 3 % more).
 //   rows  1 x 4096: 3.8
-//   32 x 64, four teams    128 x 4096: 9.0; 64 x 64: 12.2; 64 x 128: 14.8
-//   64 x 64, three teams   333 x 2050 (K = 7200): 21.2; 32 x 64: 28.0; 64 x 128: 27.0
-//   64 x 128, two teams    2048 x 4096: 68.6
-//   128 x 128              2048 x 4096: 58.7; 2048 x 14336: 202, 64 x 128: 235
-// 128 x 256 takes 61.1 and 233, two of 128 x 128's rounds and more: it is not here.
+//   32 x 64, four teams    128 x 4096: 8.6; 64 x 64: 11.7; 64 x 128: 14.5
+//   64 x 64, three teams   333 x 2050 (K = 7200): 20.4; 32 x 64: 26.9; 64 x 128: 26.2
+//   64 x 128, two teams    700 x 4096: 30.3; 64 x 64: 35.3
+//   128 x 128              700 x 4096: 27.1; 2048 x 4096: 61.6, 64 x 128: 71.4;
+//                          2048 x 14336: 208, 64 x 128: 243
+// 128 x 256 takes two of 128 x 128's rounds and more (2048 x 4096 4 %, 2048 x 14336
+// 15 %): it is not here.
 // (An activation row has 256 bytes a step: LDS holds no two of the largest tile.)
 // Against the best of the four for R from 40 to 2048, N from 2048 to 14336 and K from
 // 1024 to 14336 (51 sizes) the choice takes at most 7 % longer.
